@@ -409,6 +409,145 @@ la_status lora_output_delta(const void* o, const void* A_o, int64_t a_agent_stri
                             int32_t d_out, int32_t r, float lora_scale, la_dtype dt,
                             la_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Drafted trees: verifying several drafted tokens of every agent at once.
+ * ------------------------------------------------------------------------
+ * One layer of a verification step is lora_grouped_delta (the agents'
+ * projections), lora_qk_norm_rope (queries rotated, the drafted tokens' base
+ * rows cached), lr_cache_append (their LR rows), lora_attn_tree, and
+ * lora_grouped_delta again (the output projection).
+ *
+ * Sequence s has a committed length C = kv_len[s] >= 0 and n_trees trees of
+ * up to n drafted tokens (nodes): one tree shared by its agents (n_trees = 1)
+ * or one for each agent (n_trees = n_agents; agent a uses tree a).  Node j of
+ * tree t has
+ *   cache row  C + t * n + j           (base and LR caches),
+ *   position   C + depth(j), depth(j) the number of its ancestors,
+ * and sees rows [0, C), its ancestors and itself. */
+#define LA_TREE_MAX_NODES 64
+typedef struct {
+  /* Device int32 [n_seqs][n_trees][n]: parent[j] in [-1, j), -1 for a child of
+   * the committed context.  NULL: a chain, node j's parent is j - 1. */
+  const int32_t* parent;
+  /* Device int32 [n_seqs][n_trees]: nodes in use, in [0, n]; nodes at or past
+   * it are neither read as keys nor written.  NULL: all n. */
+  const int32_t* tree_len;
+  int32_t n_trees;
+} la_tree_args;
+
+/*
+ * lora_attn_tree -- attention of the drafted nodes' queries over the committed
+ * context and their own branch, with the agents' low-rank deltas as in
+ * lora_attn_prefill (K^a and V^a of the header's top, the key delta of a
+ * drafted row rotated at the node's position).
+ *
+ * args: as lora_attn_prefill, with n_q_tokens = n in [1, LA_TREE_MAX_NODES]
+ * nodes a tree, q and out [n_seqs][n_agents][n][n_q_heads][d], and
+ *   kv_len      device int32 [n_seqs], the committed lengths (0 is allowed);
+ *   max_kv_len  host bound: kv_len[s] + n_trees * n <= max_kv_len <= L_max;
+ *   B_k         may be NULL: keys without a low-rank part (LoRA on queries
+ *               and values only, or keys normed by lora_qk_norm_rope, whose
+ *               norm does not split into base and delta).
+ * q_pos0 is ignored; value_path must be LA_VALUE_REORDERED, key_pos0 0 and
+ * row_stats NULL.  The nodes' base K (rotated), base V and LR rows must be in
+ * the caches.  Cache rows no node sees may hold anything, NaN included; the
+ * rows of a tree's own nodes must be finite.  Outputs of nodes at or past
+ * tree_len are left as they were.
+ * On the tensor cores (bf16, head_dim 128) the scores take queries and keys in
+ * fp16 as lora_attn_prefill does (below 65504 in magnitude), except with B_k
+ * NULL, where they stay bf16.  No workspace: the key splits of a block are a
+ * thread-block cluster.
+ * Errors: as lora_attn_prefill; LA_ERR_INVALID_ARG for a null tree, n_trees
+ * neither 1 nor n_agents or n outside [1, LA_TREE_MAX_NODES];
+ * LA_ERR_CAPACITY (max_kv_len > L_max or < n_trees * n); LA_ERR_UNSUPPORTED
+ * for a GQA group above 64.  On the device, a kv_len[s] outside
+ * [0, max_kv_len - n_trees * n] (LA_DEV_KV_LEN), a parent or tree_len out of
+ * range (LA_DEV_TREE) leave that tree's outputs unwritten.
+ */
+la_status lora_attn_tree(const la_attn_args* args, const la_tree_args* tree, la_stream_t stream);
+
+/* Arguments of lora_qk_norm_rope. */
+typedef struct {
+  int32_t n_seqs, n_agents, n_tokens, n_q_heads, n_kv_heads, head_dim; /* d: 64 or 128 */
+  float eps;            /* >= 0, added to the mean square */
+  double rope_base;
+  /* Queries before norm and rotation: element (s, a, j, h, c) at
+   * s*q_seq_stride + a*q_agent_stride + j*q_tok_stride + h*d + c.  NULL: none. */
+  const void* q;
+  int64_t q_seq_stride, q_agent_stride, q_tok_stride;
+  void* q_out;          /* [n_seqs][n_agents][n_tokens][n_q_heads][d]; may be q itself */
+  /* The new tokens' base keys and values, element (s, t, j, h, c) at
+   * s*kv_in_seq_stride + t*kv_in_tree_stride + j*kv_in_tok_stride + h*d + c,
+   * t < n_trees.  k NULL: only queries; v NULL: no value rows. */
+  const void* k;
+  const void* v;
+  int64_t kv_in_seq_stride, kv_in_tree_stride, kv_in_tok_stride;
+  const void* w_q;      /* norm weights [d]; NULL: no norm, rotation only */
+  const void* w_k;
+  void* k_base;         /* base caches, as la_attn_args; NULL exactly where k / v is */
+  void* v_base;
+  int64_t L_max, kv_seq_stride, kv_head_stride, kv_tok_stride;
+  const int32_t* kv_len; /* device [n_seqs]: committed lengths, >= 0 */
+  int64_t max_kv_len;   /* host bound: kv_len[s] + n_trees * n_tokens <= max_kv_len <= L_max */
+  la_dtype dtype;       /* of every tensor */
+} la_qk_args;
+
+/*
+ * lora_qk_norm_rope -- per-head norm of new queries and keys, the rotation,
+ * and the cache rows, in one pass:
+ *   q_out[s][a][j][h] = RoPE_pos( norm(q[s][a][j][h], w_q) )
+ *   k_base[s][h][row] = RoPE_pos( norm(k[s][t][j][h], w_k) )
+ *   v_base[s][h][row] = v[s][t][j][h]
+ * with norm(x, w) = x / sqrt(mean(x^2) + eps) * w over the head dimension
+ * (statistics in fp32), RoPE as for the keys of the caches, and rows and
+ * positions of the tree above; tree NULL is one chain per sequence: token j in
+ * row and at position kv_len[s] + j (a decode token, or a prompt chunk of any
+ * length).  Rows of tokens at or past tree_len are left as they were, in
+ * q_out and in the caches.
+ * Errors: LA_ERR_INVALID_ARG (null, misaligned or inconsistent pointers, bad
+ * sizes, strides not multiples of 16 bytes), LA_ERR_UNSUPPORTED (head_dim, a
+ * tree with parents of more than LA_TREE_MAX_NODES tokens, grid limits),
+ * LA_ERR_CAPACITY.  Device checks as lora_attn_tree.
+ */
+la_status lora_qk_norm_rope(const la_qk_args* args, const la_tree_args* tree, la_stream_t stream);
+
+/* Arguments of lora_grouped_delta. */
+typedef struct {
+  int32_t n_tokens;     /* rows of x, y and out */
+  int32_t hidden;       /* columns of x */
+  int32_t n_out;        /* columns of y and out */
+  int32_t r;            /* 8, 16, 32 or 64 */
+  int32_t n_agents, n_segs;
+  float lora_scale;
+  const void* x;        /* [n_tokens][hidden], row stride ldx */
+  int64_t ldx;
+  const void* A;        /* agent a's [hidden][r] at A + a * a_agent_stride; stride 0: one A */
+  int64_t a_agent_stride;
+  const void* B;        /* [n_agents][r][n_out], contiguous */
+  const void* y;        /* [n_tokens][n_out], row stride ldy */
+  int64_t ldy;
+  void* out;            /* row stride ldo; y itself (with ldo = ldy), or no overlap with any input */
+  int64_t ldo;
+  const int32_t* seg_start; /* device [n_segs + 1], non-decreasing, within [0, n_tokens] */
+  const int32_t* seg_agent; /* device [n_segs]: the segment's agent, or -1: no adapter */
+  la_dtype dtype;
+} la_grouped_args;
+
+/*
+ * lora_grouped_delta -- the low-rank product of tokens grouped by agent in
+ * ragged segments (agents with different numbers of tokens, some with none):
+ * for every row i of segment g, seg_start[g] <= i < seg_start[g+1], a = seg_agent[g]:
+ *   out[i] = y[i] + s * ( x[i] A_a ) B_a          (a = -1: out[i] = y[i])
+ * The segment form of lora_output_delta, for any projection.  Several segments
+ * may name one agent.  Rows in no segment are left as they were.  x A_a stays in
+ * fp32 on chip (the tensor cores take it as two bf16 terms).
+ * Errors: LA_ERR_INVALID_ARG (null or misaligned pointers, bad sizes, row
+ * strides or hidden / n_out not multiples of 16 bytes), LA_ERR_UNSUPPORTED (r,
+ * grid limits).  A seg_start or seg_agent out of range on the device
+ * (LA_DEV_SEGMENT) leaves out unwritten.
+ */
+la_status lora_grouped_delta(const la_grouped_args* args, la_stream_t stream);
+
 /*
  * lora_materialize_agent_kv -- the non-shared baseline's caches.
  *
@@ -449,11 +588,15 @@ la_status lora_attn_decode_static_scratch(const la_attn_args* args, la_stream_t 
  *                     held a value no call leaves there (a workspace not
  *                     zero-filled before its first use); that unit's output
  *                     is not to be trusted and may be left unwritten
+ *   LA_DEV_TREE       a drafted tree's parent or tree_len out of range
+ *   LA_DEV_SEGMENT    a seg_start or seg_agent out of range
  * No check traps: every kernel returns and the context stays usable.
  */
 #define LA_DEV_KV_LEN 1
 #define LA_DEV_PIPE_WAIT 2
 #define LA_DEV_MERGE_WAIT 4
+#define LA_DEV_TREE 8
+#define LA_DEV_SEGMENT 16
 la_status la_device_check(void);
 la_status la_device_check_word(int32_t* word);
 

@@ -309,3 +309,91 @@ def combine_slices(outs, Ms, Ls) -> np.ndarray:
     w = np.where(Ls > 0, np.exp2(Ms - np.where(np.isfinite(Mx), Mx, 0.0)[None]) * Ls, 0.0)
     tot = w.sum(axis=0)
     return np.where(tot[..., None] > 0, (w[..., None] * outs).sum(axis=0) / np.where(tot > 0, tot, 1.0)[..., None], 0.0)
+
+
+# ----------------------------------------------------------------------------
+# Drafted trees: several drafted tokens of every agent verified at once
+# ----------------------------------------------------------------------------
+# The pages decode one token a step; a verification step attends a tree of
+# drafted tokens instead.  Node j of tree t of a sequence with committed length
+# C sits in cache row C + t n + j, at position C + depth(j), and sees rows
+# [0, C), its ancestors and itself.  A chain of one node is the plain decode,
+# a chain of n nodes the prefill of n tokens.
+def tree_chain(parent, j: int):
+    """Node j's ancestors from the root down, j itself last."""
+    out = [j]
+    while parent[out[-1]] >= 0:
+        out.append(int(parent[out[-1]]))
+    return out[::-1]
+
+
+def tree_attention(k_base, v_base, lr, B_k, B_v, q, kv_len, parent, tree_len, *, n_trees: int,
+                   lora_scale: float, softmax_scale: float, rope_base: float):
+    """Every agent's outputs for its tree's nodes, as a list of tuples
+    (seq, agent, out [m, n_q, d], pv [m, n_q, d], qk [m, n_q], qd [m, n_q]):
+    out the attention of the m live nodes, and for error bounds pv = P |V^a|,
+    qk = max over visible keys of |q| . |K^a| and qd the same of the rotated
+    key delta.
+
+    k_base, v_base [n_seqs, n_kv, L, d]; lr [n_seqs, L, 2r] or one per agent;
+    B_k [n_agents, r, n_kv*d] or None; q [n_seqs, n_agents, n, n_q, d];
+    parent [n_seqs, n_trees, n] or None (chains); tree_len [n_seqs, n_trees] or None."""
+    n_seqs, n_agents, n, n_q, d = q.shape
+    n_kv, r = k_base.shape[1], lr.shape[-1] // 2
+    g = n_q // n_kv
+    res = []
+    for s_ in range(n_seqs):
+        C = int(kv_len[s_])
+        for a in range(n_agents):
+            t = a if n_trees > 1 else 0
+            m = n if tree_len is None else int(tree_len[s_, t])
+            par = [j - 1 for j in range(n)] if parent is None else [int(x) for x in parent[s_, t]]
+            chains = [tree_chain(par, j) for j in range(m)]
+            rows = np.concatenate([np.arange(C), C + t * n + np.arange(m)]).astype(int)
+            pos = np.concatenate([np.arange(C), [C + len(c) - 1 for c in chains]])
+            see = np.zeros((m, C + m), dtype=bool)
+            see[:, :C] = True
+            for j, c in enumerate(chains):
+                see[j, [C + i for i in c]] = True
+            lrs = _np64((lr[a, s_] if lr.ndim == 4 else lr[s_])[rows])
+            out, pv = np.zeros((m, n_q, d)), np.zeros((m, n_q, d))
+            qk, qd = np.zeros((m, n_q)), np.zeros((m, n_q))
+            for h in range(n_kv if m else 0):
+                cols = slice(h * d, (h + 1) * d)
+                base = _np64(k_base[s_, h][rows])
+                delta = np.zeros_like(base)
+                if B_k is not None:
+                    delta = rope(lora_scale * (lrs[:, :r] @ _np64(B_k[a])[:, cols]), pos, rope_base)
+                K = base + delta
+                V = agent_values(v_base[s_, h][rows], lrs[:, r:], _np64(B_v[a])[:, cols], lora_scale)
+                for hh in range(h * g, (h + 1) * g):
+                    qq = _np64(q[s_, a, :m, hh])
+                    z = np.where(see, (qq @ K.T) * softmax_scale, -np.inf)
+                    e = np.exp(z - z.max(axis=1, keepdims=True))
+                    P = e / e.sum(axis=1, keepdims=True)
+                    out[:, hh] = P @ V
+                    pv[:, hh] = P @ np.abs(V)
+                    qk[:, hh] = np.where(see, np.abs(qq) @ np.abs(K).T, 0).max(axis=1)
+                    qd[:, hh] = np.where(see, np.abs(qq) @ np.abs(delta).T, 0).max(axis=1)
+            res.append((s_, a, out, pv, qk, qd))
+    return res
+
+
+def head_norm(x, w, eps: float) -> np.ndarray:
+    """x / sqrt(mean(x^2) + eps) * w over the last dimension; w None: x itself."""
+    x = _np64(x)
+    if w is None:
+        return x
+    return x / np.sqrt((x * x).mean(axis=-1, keepdims=True) + eps) * _np64(w)
+
+
+def grouped_delta(x, A, B, y, seg_start, seg_agent, lora_scale: float) -> np.ndarray:
+    """y + s (x A_a) B_a for the rows of every segment of agent a (a < 0: y);
+    A [hidden, r] or [n_agents, hidden, r].  Rows in no segment keep y."""
+    out = _np64(y).copy()
+    for g in range(len(seg_agent)):
+        lo, hi, a = int(seg_start[g]), int(seg_start[g + 1]), int(seg_agent[g])
+        if a >= 0:
+            Aa = _np64(A) if A.ndim == 2 else _np64(A[a])
+            out[lo:hi] += lora_scale * ((_np64(x[lo:hi]) @ Aa) @ _np64(B[a]))
+    return out

@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include "la_internal.cuh"
+#include "tree.cuh"
 
 namespace la {
 
@@ -32,8 +33,14 @@ bool bf16_prefill_supported(const AttnParams& p);
 bool bf16_prefill_per_tile_supported(const AttnParams& p);
 cudaError_t launch_prefill_bf16(const AttnParams& p, la_dtype out, cudaStream_t st);
 bool bf16_append_supported(int64_t H, int r);
+bool attn_tree_simt_supported(const AttnParams& p);
+cudaError_t launch_attn_tree_simt(const AttnParams& p, const TreeParams& tp, la_dtype io, la_dtype out,
+                                  cudaStream_t st);
 
 namespace {
+
+// what check_attn checks the arguments for
+enum Mode { kPrefill = 0, kDecode = 1, kTree = 2 };
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t esize(la_dtype t) { return t == LA_F32 ? 4 : 2; }
@@ -41,8 +48,9 @@ bool dtype_ok(int t) { return t == LA_F32 || t == LA_BF16; }
 bool rank_ok(int r) { return r == 8 || r == 16 || r == 32 || r == 64; }
 bool stride_ok(int64_t s, la_dtype t) { return s > 0 && ((s * (int64_t)esize(t)) % 16) == 0; }
 
-// Checks common to prefill and decode; fills p on success.
-la_status check_attn(const la_attn_args* a, int decode, AttnParams* p) {
+// Checks common to prefill, decode and the drafted trees; fills p on success.
+la_status check_attn(const la_attn_args* a, int mode, AttnParams* p) {
+  const bool decode = mode == kDecode, tree = mode == kTree;
   if (!a) return LA_ERR_INVALID_ARG;
   if (!dtype_ok(a->io_dtype) || !dtype_ok(a->out_dtype)) return LA_ERR_INVALID_ARG;
   if (a->n_seqs < 0 || a->n_agents < 1 || a->n_q_heads < 1 || a->n_kv_heads < 1)
@@ -54,7 +62,7 @@ la_status check_attn(const la_attn_args* a, int decode, AttnParams* p) {
     return LA_ERR_INVALID_ARG;
   if (!isfinite(a->rope_base) || !(a->rope_base > 1.0)) return LA_ERR_INVALID_ARG;
   if (a->L_max < 1) return LA_ERR_INVALID_ARG;
-  if (!a->k_base || !a->v_base || !a->lr_cache || !a->B_k || !a->B_v || !a->q || !a->out)
+  if (!a->k_base || !a->v_base || !a->lr_cache || (!a->B_k && !tree) || !a->B_v || !a->q || !a->out)
     return LA_ERR_INVALID_ARG;
   if (!aligned16(a->k_base) || !aligned16(a->v_base) || !aligned16(a->lr_cache) ||
       !aligned16(a->B_k) || !aligned16(a->B_v) || !aligned16(a->q) || !aligned16(a->out))
@@ -73,8 +81,13 @@ la_status check_attn(const la_attn_args* a, int decode, AttnParams* p) {
   if (a->key_pos0 < 0 || (reinterpret_cast<uintptr_t>(a->row_stats) & 7u) != 0) return LA_ERR_INVALID_ARG;
   if (!decode && (a->key_pos0 != 0 || a->row_stats)) return LA_ERR_UNSUPPORTED;   // decode only
   const int g = a->n_q_heads / a->n_kv_heads;
-  if ((int64_t)a->n_agents * g > kMaxRowsSimt) return LA_ERR_UNSUPPORTED;
-  if (decode) {
+  if (!tree && (int64_t)a->n_agents * g > kMaxRowsSimt) return LA_ERR_UNSUPPORTED;
+  if (tree) {
+    if (a->n_q_tokens < 1 || a->n_q_tokens > kTreeMaxNodes) return LA_ERR_INVALID_ARG;
+    if (!a->kv_len || a->max_kv_len < 1) return LA_ERR_INVALID_ARG;
+    if (a->max_kv_len > a->L_max) return LA_ERR_CAPACITY;
+    if (a->value_path != LA_VALUE_REORDERED) return LA_ERR_UNSUPPORTED;
+  } else if (decode) {
     if (a->n_q_tokens != 1) return LA_ERR_INVALID_ARG;
     if (!a->kv_len) return LA_ERR_INVALID_ARG;
     if (a->max_kv_len < 1) return LA_ERR_INVALID_ARG;
@@ -111,7 +124,7 @@ la_status check_attn(const la_attn_args* a, int decode, AttnParams* p) {
   p->out = a->out;
   p->kv_len = a->kv_len;
   p->max_kv_len = a->max_kv_len;
-  p->q_pos0 = a->q_pos0;
+  p->q_pos0 = tree ? 0 : a->q_pos0;
   p->n_q_tokens = decode ? 1 : a->n_q_tokens;
   p->decode = decode;
   p->key_pos0 = a->key_pos0;
@@ -489,6 +502,25 @@ extern "C" la_status lora_attn_prefill(const la_attn_args* a, la_stream_t stream
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = tc ? launch_prefill_bf16(p, a->out_dtype, st)
                            : launch_attn_simt(p, a->io_dtype, a->out_dtype, st);
+  return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+extern "C" la_status lora_attn_tree(const la_attn_args* a, const la_tree_args* tree, la_stream_t stream) {
+  AttnParams p;
+  const la_status s = check_attn(a, kTree, &p);
+  if (s != LA_OK) return s;
+  if (!tree || (tree->n_trees != 1 && tree->n_trees != a->n_agents)) return LA_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(tree->parent) | reinterpret_cast<uintptr_t>(tree->tree_len) |
+        reinterpret_cast<uintptr_t>(a->kv_len)) & 3u) != 0)
+    return LA_ERR_INVALID_ARG;
+  if ((int64_t)tree->n_trees * a->n_q_tokens > a->max_kv_len) return LA_ERR_CAPACITY;
+  if (!attn_tree_simt_supported(p)) return LA_ERR_UNSUPPORTED;
+  if (p.n_seqs == 0) return LA_OK;
+  p.err = error_word_ptr();
+  if (!p.err) return LA_ERR_CUDA;
+  const TreeParams tp = {tree->parent, tree->tree_len, tree->n_trees, a->n_q_tokens};
+  const cudaError_t e =
+      launch_attn_tree_simt(p, tp, a->io_dtype, a->out_dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

@@ -23,14 +23,16 @@ LA_ERR_WORKSPACE, LA_ERR_CUDA, LA_ERR_DEVICE_CHECK, LA_ERR_SCRATCH_LIMIT = 4, 5,
 LA_STATIC_SCRATCH_BYTES = 4 << 20
 LA_F32, LA_BF16 = 0, 1
 LA_VALUE_REORDERED, LA_VALUE_REORDERED_GENERIC, LA_VALUE_PER_TILE, LA_VALUE_PER_TILE_GENERIC = 0, 1, 2, 3
-LA_DEV_KV_LEN, LA_DEV_PIPE_WAIT, LA_DEV_MERGE_WAIT = 1, 2, 4
+LA_DEV_KV_LEN, LA_DEV_PIPE_WAIT, LA_DEV_MERGE_WAIT, LA_DEV_TREE, LA_DEV_SEGMENT = 1, 2, 4, 8, 16
+LA_TREE_MAX_NODES = 64
 
 EXPORTED = ("la_status_string", "lr_cache_append", "lora_attn_prefill", "lora_attn_decode",
             "lora_attn_decode_workspace_bytes", "la_device_check",
             "lora_attn_decode_static_scratch", "lora_materialize_agent_kv",
             "lr_cache_append_agents", "lora_query_expand", "lora_output_delta",
             "la_device_check_word", "lora_decode_step_host", "lora_attn_decode_step",
-            "lora_attn_decode_combine")
+            "lora_attn_decode_combine", "lora_attn_tree", "lora_qk_norm_rope",
+            "lora_grouped_delta")
 
 
 class LoraAttnError(RuntimeError):
@@ -64,6 +66,50 @@ class AttnArgs(ctypes.Structure):
         ("value_path", ctypes.c_int32),
         ("key_pos0", ctypes.c_int64),
         ("row_stats", ctypes.c_void_p),
+    ]
+
+
+class TreeArgs(ctypes.Structure):
+    """Mirror of la_tree_args."""
+
+    _fields_ = [("parent", ctypes.c_void_p), ("tree_len", ctypes.c_void_p),
+                ("n_trees", ctypes.c_int32)]
+
+
+class QkArgs(ctypes.Structure):
+    """Mirror of la_qk_args."""
+
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("n_agents", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+        ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("rope_base", ctypes.c_double),
+        ("q", ctypes.c_void_p), ("q_seq_stride", ctypes.c_int64),
+        ("q_agent_stride", ctypes.c_int64), ("q_tok_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("kv_in_seq_stride", ctypes.c_int64), ("kv_in_tree_stride", ctypes.c_int64),
+        ("kv_in_tok_stride", ctypes.c_int64),
+        ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p),
+        ("k_base", ctypes.c_void_p), ("v_base", ctypes.c_void_p),
+        ("L_max", ctypes.c_int64), ("kv_seq_stride", ctypes.c_int64),
+        ("kv_head_stride", ctypes.c_int64), ("kv_tok_stride", ctypes.c_int64),
+        ("kv_len", ctypes.c_void_p), ("max_kv_len", ctypes.c_int64), ("dtype", ctypes.c_int),
+    ]
+
+
+class GroupedArgs(ctypes.Structure):
+    """Mirror of la_grouped_args."""
+
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("n_out", ctypes.c_int32),
+        ("r", ctypes.c_int32), ("n_agents", ctypes.c_int32), ("n_segs", ctypes.c_int32),
+        ("lora_scale", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+        ("A", ctypes.c_void_p), ("a_agent_stride", ctypes.c_int64), ("B", ctypes.c_void_p),
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+        ("seg_start", ctypes.c_void_p), ("seg_agent", ctypes.c_void_p), ("dtype", ctypes.c_int),
     ]
 
 
@@ -123,6 +169,14 @@ def _load() -> ctypes.CDLL:
     lib.lora_attn_decode_combine.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                              ctypes.c_int64, ctypes.c_int32, ctypes.c_int,
                                              ctypes.c_void_p, ctypes.c_void_p]
+    lib.lora_attn_tree.restype = ctypes.c_int
+    lib.lora_attn_tree.argtypes = [ctypes.POINTER(AttnArgs), ctypes.POINTER(TreeArgs),
+                                   ctypes.c_void_p]
+    lib.lora_qk_norm_rope.restype = ctypes.c_int
+    lib.lora_qk_norm_rope.argtypes = [ctypes.POINTER(QkArgs), ctypes.POINTER(TreeArgs),
+                                      ctypes.c_void_p]
+    lib.lora_grouped_delta.restype = ctypes.c_int
+    lib.lora_grouped_delta.argtypes = [ctypes.POINTER(GroupedArgs), ctypes.c_void_p]
     return lib
 
 
@@ -229,6 +283,7 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
     stride); lr [n_seqs, L_max, 2r], one LR cache shared by every agent, or
     [n_agents, n_seqs, L_max, 2r], one per agent; B_k, B_v [n_agents, r, n_kv*d];
     q, out [n_seqs, n_agents, n_tok, n_q, d] contiguous; kv_len int32 [n_seqs].
+    B_k may be None for lora_attn_tree alone (keys without a low-rank part).
     Sequence-sharded decode: key_pos0 is the position of the caches' key row 0;
     row_stats a float32 [n_seqs, n_agents, n_q, 2] tensor the decode fills
     with each row's (M, L) for lora_attn_decode_combine."""
@@ -242,7 +297,8 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
     r = lr.shape[2] // 2
     assert k_base.stride() == v_base.stride() and k_base.stride(3) == 1
     assert lr.stride(2) == 1 and lr.stride(1) == 2 * r
-    assert B_k.is_contiguous() and B_v.is_contiguous() and q.is_contiguous() and out.is_contiguous()
+    assert B_k is None or B_k.is_contiguous()
+    assert B_v.is_contiguous() and q.is_contiguous() and out.is_contiguous()
     a = AttnArgs()
     a.n_seqs, a.n_agents, a.n_q_heads, a.n_kv_heads = n_seqs, n_agents, n_q, n_kv
     a.head_dim, a.r = d, r
@@ -254,7 +310,7 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
     a.kv_seq_stride, a.kv_head_stride, a.kv_tok_stride = (k_base.stride(0), k_base.stride(1),
                                                           k_base.stride(2))
     a.lr_cache, a.lr_seq_stride = lr.data_ptr(), lr.stride(0)
-    a.B_k, a.B_v = B_k.data_ptr(), B_v.data_ptr()
+    a.B_k, a.B_v = (B_k.data_ptr() if B_k is not None else None), B_v.data_ptr()
     a.q, a.out = q.data_ptr(), out.data_ptr()
     a.kv_len = kv_len.data_ptr() if kv_len is not None else None
     a.max_kv_len = max_kv_len
@@ -268,6 +324,7 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
         assert row_stats.dtype == torch.float32 and row_stats.is_contiguous()
         assert row_stats.numel() == 2 * n_seqs * n_agents * n_q
     a.row_stats = row_stats.data_ptr() if row_stats is not None else None
+    a.device = q.device.index
     return a
 
 
@@ -366,6 +423,203 @@ def lora_materialize_agent_kv(args: AttnArgs, k_out: torch.Tensor, v_out: torch.
 def lora_attn_prefill(args: AttnArgs, stream=None) -> None:
     st = lib.lora_attn_prefill(ctypes.byref(args), _stream(stream))
     _check(st, "lora_attn_prefill")
+
+
+def _same_device(ts) -> int:
+    """The one CUDA device that holds every tensor (None entries are skipped)."""
+    devs = {t.device for t in ts if t is not None}
+    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+        raise ValueError(f"expected every tensor on one CUDA device, got {sorted(map(str, devs))}")
+    return next(iter(devs)).index
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(device: int, stream, where: str) -> int:
+    """The stream to launch on; the arguments' device must be the current one."""
+    if torch.cuda.current_device() != device:
+        raise ValueError(f"{where}: tensors are on cuda:{device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def make_tree_args(parent: Optional[torch.Tensor], tree_len: Optional[torch.Tensor] = None, *,
+                   n_trees: Optional[int] = None) -> TreeArgs:
+    """Fill la_tree_args: drafted trees, one per sequence (n_trees = 1) or one
+    per agent.
+
+    parent int32 [n_seqs, n_trees, n], parent[.., j] in [-1, j), or None: every
+    tree is a chain; tree_len int32 [n_seqs, n_trees], nodes in use, or None: all
+    of them.  n_trees is needed only where both are None (default 1)."""
+    shape = None
+    for t, dims in ((parent, 3), (tree_len, 2)):
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+            raise ValueError(f"expected a contiguous int32 tensor of {dims} dimensions, got "
+                             f"{t.dtype} {tuple(t.shape)}")
+        if shape is not None and tuple(t.shape[:2]) != shape:
+            raise ValueError("parent and tree_len disagree on [n_seqs, n_trees]")
+        shape = tuple(t.shape[:2])
+    if shape is not None and n_trees not in (None, shape[1]):
+        raise ValueError("n_trees disagrees with parent / tree_len")
+    a = TreeArgs()
+    a.parent, a.tree_len = _ptr(parent), _ptr(tree_len)
+    a.n_trees = shape[1] if shape is not None else (1 if n_trees is None else n_trees)
+    a.n_seqs = None if shape is None else shape[0]
+    a.n = None if parent is None else parent.shape[2]
+    a.device = None if shape is None else _same_device((parent, tree_len))
+    return a
+
+
+def _check_tree(tree: TreeArgs, n_seqs: int, n: int, where: str) -> None:
+    if tree.n_seqs not in (None, n_seqs) or tree.n not in (None, n):
+        raise ValueError(f"{where}: the trees' shape [n_seqs, n_trees, n] does not fit the call's "
+                         f"n_seqs {n_seqs} and n {n}")
+
+
+def lora_attn_tree(args: AttnArgs, tree: TreeArgs, stream=None) -> None:
+    """Attention of the drafted nodes over the committed context and their own
+    branches.  args from make_args, with q and out [n_seqs, n_agents, n, n_q, d],
+    kv_len the committed lengths and max_kv_len a bound on kv_len + n_trees * n."""
+    _check_tree(tree, args.n_seqs, args.n_q_tokens, "lora_attn_tree")
+    device = getattr(args, "device", None)   # of make_args' tensors
+    if tree.device not in (None, device):
+        raise ValueError("lora_attn_tree: the trees are on another device")
+    s = _stream(stream) if device is None else _on_device(device, stream, "lora_attn_tree")
+    st = lib.lora_attn_tree(ctypes.byref(args), ctypes.byref(tree), s)
+    _check(st, "lora_attn_tree")
+
+
+def make_qk_args(q, k, v, w_q, w_k, q_out, k_base, v_base, kv_len, *, rope_base: float,
+                 max_kv_len: int, eps: float = 1e-6) -> QkArgs:
+    """Fill la_qk_args from tensors.
+
+    q [n_seqs, n_agents, n, n_q, d] (heads contiguous; sequence, agent and token
+    strides free: slices of a fused projection's output will do) with q_out of
+    that shape, contiguous, or both None; k, v [n_seqs, n_trees, n, n_kv, d] the
+    same way, of equal strides, with the base caches k_base, v_base
+    [n_seqs, n_kv, L_max, d] of equal strides, or None; w_q, w_k [d] or None;
+    kv_len int32 [n_seqs]."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("one of q and k is needed")
+    dt = ref.dtype
+    for t in (q, k, v, w_q, w_k, q_out, k_base, v_base):
+        if t is not None and t.dtype != dt:
+            raise TypeError(f"expected every tensor of {dt}, got {t.dtype}")
+    a = QkArgs()
+    n_seqs, _, n, _, d = ref.shape
+    a.n_seqs, a.n_tokens, a.head_dim = n_seqs, n, d
+    a.n_agents = a.n_q_heads = a.n_kv_heads = 1
+    a.eps, a.rope_base = eps, rope_base
+    if (q is None) != (q_out is None) or (k is None) != (k_base is None) or \
+            (v is None) != (v_base is None):
+        raise ValueError("q and q_out, k and k_base, v and v_base come together")
+
+    def heads(t):
+        if t.dim() != 5 or t.shape[0] != n_seqs or t.shape[2] != n or t.shape[4] != d or \
+                t.stride(4) != 1 or (t.shape[3] > 1 and t.stride(3) != d):
+            raise ValueError("expected [n_seqs, ., n, heads, d] with contiguous heads, got "
+                             f"{tuple(t.shape)} with strides {t.stride()}")
+
+    if q is not None:
+        heads(q)
+        if q_out.shape != q.shape or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous, of q's shape")
+        a.n_agents, a.n_q_heads = q.shape[1], q.shape[3]
+        a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
+        a.q_seq_stride, a.q_agent_stride, a.q_tok_stride = q.stride()[:3]
+    a.n_trees = None
+    if k is not None:
+        heads(k)
+        a.n_trees = k.shape[1]
+        if q is None:
+            a.n_agents = k.shape[1]
+        a.n_kv_heads = k.shape[3]
+        a.k, a.v = k.data_ptr(), _ptr(v)
+        a.kv_in_seq_stride, a.kv_in_tree_stride, a.kv_in_tok_stride = k.stride()[:3]
+        if k_base.dim() != 4 or k_base.shape[:2] != (n_seqs, a.n_kv_heads) or \
+                k_base.shape[3] != d or k_base.stride(3) != 1:
+            raise ValueError("k_base must be [n_seqs, n_kv, L_max, d] with a unit last stride")
+        if v is not None and (v.shape != k.shape or v.stride() != k.stride() or
+                              v_base.shape != k_base.shape or v_base.stride() != k_base.stride()):
+            raise ValueError("v and v_base must have the shapes and strides of k and k_base")
+        a.k_base, a.v_base = k_base.data_ptr(), _ptr(v_base)
+        a.L_max = k_base.shape[2]
+        a.kv_seq_stride, a.kv_head_stride, a.kv_tok_stride = k_base.stride()[:3]
+    elif v is not None:
+        raise ValueError("v needs k")
+    else:
+        a.L_max = max(1, max_kv_len)
+    for w in (w_q, w_k):
+        if w is not None and (w.shape != (d,) or not w.is_contiguous()):
+            raise ValueError("norm weights are contiguous [d]")
+    a.w_q, a.w_k = _ptr(w_q), _ptr(w_k)
+    if kv_len.dtype != torch.int32 or kv_len.shape != (n_seqs,) or not kv_len.is_contiguous():
+        raise ValueError("kv_len must be int32 [n_seqs]")
+    a.kv_len, a.max_kv_len, a.dtype = kv_len.data_ptr(), max_kv_len, _dt(ref)
+    a.device = _same_device((q, k, v, w_q, w_k, q_out, k_base, v_base, kv_len))
+    return a
+
+
+def lora_qk_norm_rope(args: QkArgs, tree: Optional[TreeArgs] = None, stream=None) -> None:
+    """Norm and rotate new queries and keys per head and write the cache rows
+    (args from make_qk_args); tree None: one chain per sequence from kv_len on."""
+    if tree is not None:
+        _check_tree(tree, args.n_seqs, args.n_tokens, "lora_qk_norm_rope")
+        if tree.device not in (None, args.device):
+            raise ValueError("lora_qk_norm_rope: the trees are on another device")
+    if args.n_trees is not None and args.n_trees != (1 if tree is None else tree.n_trees):
+        raise ValueError(f"lora_qk_norm_rope: k has {args.n_trees} trees of rows")
+    s = _on_device(args.device, stream, "lora_qk_norm_rope")
+    st = lib.lora_qk_norm_rope(ctypes.byref(args), None if tree is None else ctypes.byref(tree), s)
+    _check(st, "lora_qk_norm_rope")
+
+
+def make_grouped_args(x, A, B, y, out, seg_start, seg_agent, *, lora_scale: float) -> GroupedArgs:
+    """Fill la_grouped_args from tensors.
+
+    x [n_tokens, hidden], y and out [n_tokens, n_out] (unit last strides; out may
+    be y); A [hidden, r] shared, or [n_agents, hidden, r]; B [n_agents, r, n_out]
+    contiguous; seg_start int32 [n_segs + 1], seg_agent int32 [n_segs]."""
+    T, H = x.shape
+    n_agents, r, N = B.shape
+    if y.shape != (T, N) or out.shape != (T, N) or tuple(A.shape[-2:]) != (H, r) or \
+            A.dim() not in (2, 3) or (A.dim() == 3 and A.shape[0] != n_agents):
+        raise ValueError("shapes of x, A, B, y and out do not fit")
+    if not (x.stride(1) == y.stride(1) == out.stride(1) == 1) or not B.is_contiguous() or \
+            A.stride(-1) != 1 or A.stride(-2) != r:
+        raise ValueError("x, y and out need unit last strides, B and each A must be contiguous")
+    for t in (A, B, y, out):
+        if t.dtype != x.dtype:
+            raise TypeError(f"expected every tensor of {x.dtype}, got {t.dtype}")
+    n_segs = seg_agent.numel()
+    if seg_start.dtype != torch.int32 or seg_agent.dtype != torch.int32 or \
+            seg_start.shape != (n_segs + 1,) or seg_agent.dim() != 1 or \
+            not seg_start.is_contiguous() or not seg_agent.is_contiguous():
+        raise ValueError("seg_start is int32 [n_segs + 1], seg_agent int32 [n_segs]")
+    a = GroupedArgs()
+    a.n_tokens, a.hidden, a.n_out, a.r, a.n_agents, a.n_segs = T, H, N, r, n_agents, n_segs
+    a.lora_scale = lora_scale
+    a.x, a.ldx = x.data_ptr(), x.stride(0) if T > 1 else H
+    a.A, a.a_agent_stride = A.data_ptr(), (A.stride(0) if A.dim() == 3 else 0)
+    a.B = B.data_ptr()
+    a.y, a.ldy = y.data_ptr(), y.stride(0) if T > 1 else N
+    a.out, a.ldo = out.data_ptr(), out.stride(0) if T > 1 else N
+    a.seg_start, a.seg_agent, a.dtype = seg_start.data_ptr(), seg_agent.data_ptr(), _dt(x)
+    a.device = _same_device((x, A, B, y, out, seg_start, seg_agent))
+    return a
+
+
+def lora_grouped_delta(args: GroupedArgs, stream=None) -> None:
+    """out = y + s (x A_a) B_a over ragged segments of tokens grouped by agent
+    (args from make_grouped_args)."""
+    s = _on_device(args.device, stream, "lora_grouped_delta")
+    st = lib.lora_grouped_delta(ctypes.byref(args), s)
+    _check(st, "lora_grouped_delta")
 
 
 def la_device_check() -> int:
