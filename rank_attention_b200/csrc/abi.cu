@@ -34,8 +34,9 @@ bool bf16_prefill_per_tile_supported(const AttnParams& p);
 cudaError_t launch_prefill_bf16(const AttnParams& p, la_dtype out, cudaStream_t st);
 bool bf16_append_supported(int64_t H, int r);
 bool attn_tree_simt_supported(const AttnParams& p);
-cudaError_t launch_attn_tree_simt(const AttnParams& p, const TreeParams& tp, la_dtype io, la_dtype out,
-                                  cudaStream_t st);
+cudaError_t launch_attn_tree_simt(const AttnParams& p, const TreeParams& tp, la_dtype out, cudaStream_t st);
+bool attn_tree_bf16_supported(const AttnParams& p, const TreeParams& tp);
+cudaError_t launch_attn_tree_bf16(const AttnParams& p, const TreeParams& tp, la_dtype out, cudaStream_t st);
 
 namespace {
 
@@ -514,13 +515,15 @@ extern "C" la_status lora_attn_tree(const la_attn_args* a, const la_tree_args* t
         reinterpret_cast<uintptr_t>(a->kv_len)) & 3u) != 0)
     return LA_ERR_INVALID_ARG;
   if ((int64_t)tree->n_trees * a->n_q_tokens > a->max_kv_len) return LA_ERR_CAPACITY;
-  if (!attn_tree_simt_supported(p)) return LA_ERR_UNSUPPORTED;
+  const TreeParams tp = {tree->parent, tree->tree_len, tree->n_trees, a->n_q_tokens};
+  const bool bf16 = a->io_dtype == LA_BF16;
+  if (!(bf16 ? attn_tree_bf16_supported(p, tp) : attn_tree_simt_supported(p))) return LA_ERR_UNSUPPORTED;
   if (p.n_seqs == 0) return LA_OK;
   p.err = error_word_ptr();
   if (!p.err) return LA_ERR_CUDA;
-  const TreeParams tp = {tree->parent, tree->tree_len, tree->n_trees, a->n_q_tokens};
-  const cudaError_t e =
-      launch_attn_tree_simt(p, tp, a->io_dtype, a->out_dtype, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = bf16 ? launch_attn_tree_bf16(p, tp, a->out_dtype, st)
+                             : launch_attn_tree_simt(p, tp, a->out_dtype, st);
   return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

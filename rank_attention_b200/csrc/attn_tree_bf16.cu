@@ -1,0 +1,866 @@
+// Attention of drafted trees on the tcgen05 tensor cores (bf16 storage, fp32
+// accumulation in TMEM).
+//
+// One CTA = 128 query rows (nodes x the GQA group's heads, and without a key
+// delta the agents too: their keys are the same then) of one (sequence, KV
+// head), and one split of the keys; the splits of a block are a thread-block
+// cluster and merge over distributed shared memory.  Keys stream in tiles of
+// 128: the committed context, then one tile with the tree's own nodes.  Per tile
+//   dK  = LRk B_k^a                     tcgen05, in quarters of 16 frequencies
+//   K^a = K_base + s R(k0) R(j) dK      CUDA cores, in fp16 over K_base
+//   S   = Q K^a^T                       tcgen05, Q (fp16) read from TMEM
+//   P   = exp2(S log2e scale - m)       CUDA cores, bf16 to TMEM
+//   O  += P V_base,  O_lr += P LRv      tcgen05, P read from TMEM
+// and once per row out = (O + s O_lr B_v^a) / l.  R(j) turns by the key's
+// offset in its tile, or by a node's depth in the drafted tile (k0 = C there).
+// Without a key delta (KEYS = false) K_base is the operand as it lies, in bf16,
+// and the scores are double-buffered, P lying over the scores it came from.
+//
+// Warps: eight softmax warps (two per TMEM sub-partition, 64 keys each), eight
+// build warps (16 keys each), and one warp each to issue S and P V, to load, to
+// issue dK (its quarters ping-pong with the build), and to form the anchors
+// s R(k0) in fp64.  The running maximum is rescaled lazily (O and l corrected
+// only when a row's maximum grows by more than 2^8).
+#include <cmath>
+
+#include "attn_tc_common.cuh"
+#include "bf16_common.cuh"
+#include "la_internal.cuh"
+#include "ptx.cuh"
+#include "tree.cuh"
+
+namespace la {
+namespace {
+
+constexpr int KT = 128;    // keys per tile
+constexpr int QM = 128;    // query rows per CTA
+constexpr int NSM = 8;     // softmax warps
+constexpr int kMaxSplits = 8;   // the portable cluster size
+constexpr int kPolyEvery = 4;   // every 4th pair of exponentials on the FMA pipe
+constexpr int BAR_PAIR = 2;     // named barriers 2..5: the two warps of a row block
+
+// TMEM columns.  With a key delta: Q, dK (two quarters of 32), S, P, O, O_lr;
+// without: Q, S twice (P over each), O, O_lr.
+constexpr int T_Q = 0, T_DK = 64, T_P = 256, T_O = 320, T_OL = 448, T_COLS = 512;
+
+template <int D, int R, bool KEYS>
+struct TCfg {
+  static constexpr int NB = KEYS ? 8 : 0;                       // build warps
+  static constexpr int NTHR = 32 * (NSM + NB + 4);
+  static constexpr int NQ = D / 32;                             // quarters of 16 frequencies
+  static constexpr int LR_ROWB = R * 2;
+  static constexpr uint32_t LR_LAYOUT = LR_ROWB == 128 ? 2u : (LR_ROWB == 64 ? 4u : 6u);
+  static constexpr int KV = KT * D * 2;
+  static constexpr int LRT = KT * R * 2;
+  static constexpr int KST = KV + (KEYS ? LRT : 0);             // K_base (and LRk)
+  static constexpr int VST = KV + LRT;                          // V_base and LRv
+  static constexpr int NK = 3;
+  static constexpr int NV = KEYS && D == 128 && R == 64 ? 1 : 2;   // what 227 KB leave
+  static constexpr int OFF_V = NK * KST;
+  static constexpr int OFF_BK = OFF_V + NV * VST;
+  static constexpr int OFF_MISC = OFF_BK + (KEYS ? R * D * 2 : 0);
+  // misc: anchors [3][64] float2, exchange [2][8][32] float, masks [64] u64, 32 mbarriers, TMEM slot
+  static constexpr int MISC = 1536 + 2048 + 512 + 256 + 16;
+  // at least more than half an SM's, so that one CTA is resident: two would wait
+  // for each other's TMEM across clusters
+  static constexpr int NEED = 1024 + OFF_MISC + MISC;
+  static constexpr int SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
+  // the partial (O, O_lr, m and l) over the drained stages
+  static constexpr int P_OL = QM * D * 4, P_ML = P_OL + QM * R * 4;
+  static_assert(P_ML + QM * 8 <= OFF_BK, "the partial lies over the stages");
+  static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+  // score buffers
+  __host__ __device__ static constexpr int t_s(int b) { return KEYS ? 128 : 64 + 128 * b; }
+  __host__ __device__ static constexpr int t_p(int b) { return KEYS ? T_P : 64 + 128 * b; }
+};
+
+// the split's registers: at 640 threads a CTA launches with 96 a thread
+// (61,440); 2 x 112 (softmax) + 2 x 112 (build) + 32 = 480 x 128 threads uses all
+constexpr int kLaunchRegs = 96;
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int D, int R, bool KEYS>
+__global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
+    attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ CUtensorMap tmL, const AttnParams p, const TreeParams tp,
+                        const __grid_constant__ RopeTheta rt, const int pooled) {
+  using C_ = TCfg<D, R, KEYS>;
+  constexpr int NK = C_::NK, NV = C_::NV, NQ = C_::NQ, H2 = D / 2;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t k_u = sb, v_u = sb + C_::OFF_V, bk_u = sb + C_::OFF_BK;
+  unsigned char* misc = smem + C_::OFF_MISC;
+  float2* anc = reinterpret_cast<float2*>(misc);
+  float* xch = reinterpret_cast<float*>(misc + 1536);
+  uint64_t* masks = reinterpret_cast<uint64_t*>(misc + 3584);
+  const uint32_t b0 = smem_u32(misc + 4096);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 4096 + 256);
+  __shared__ int s_bad, s_fail;
+
+  auto kfull = [&](int s) { return b0 + 8 * s; };
+  auto kfree = [&](int s) { return b0 + 24 + 8 * s; };
+  auto kaready = [&](int s) { return b0 + 48 + 8 * s; };
+  auto ancfull = [&](int s) { return b0 + 72 + 8 * s; };
+  auto vfull = [&](int s) { return b0 + 96 + 8 * s; };
+  auto vfree = [&](int s) { return b0 + 112 + 8 * s; };
+  auto dkfull = [&](int s) { return b0 + 128 + 8 * s; };
+  auto dkfree = [&](int s) { return b0 + 144 + 8 * s; };
+  auto sfull = [&](int s) { return b0 + 160 + 8 * s; };
+  auto pfull = [&](int s) { return b0 + 176 + 8 * s; };
+  const uint32_t staken = b0 + 192, pvdone = b0 + 200, qready = b0 + 208;
+
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  constexpr int W0 = NSM + C_::NB;   // MMA, loads, dK, anchors
+  const int g = p.g, n = tp.nodes;
+  const int seq = blockIdx.z, split = blockIdx.x, S = p.n_splits;
+  int y = blockIdx.y, agent0 = 0;
+  if (!pooled) {
+    agent0 = y % p.n_agents;
+    y /= p.n_agents;
+  }
+  const int kvh = y % p.n_kv, blk = y / p.n_kv;
+  const int tree = tp.n_trees > 1 ? agent0 : 0;
+  const int lra = p.lr_agent ? agent0 : 0;
+
+  // the same values, so the same branch, in the whole cluster
+  const int64_t C = p.kv_len[seq];
+  const int m = tp.tree_len ? tp.tree_len[seq * tp.n_trees + tree] : n;
+  if (C < 0 || C + (int64_t)tp.n_trees * n > p.max_kv_len) {
+    if (tid == 0) atomicOr(p.err, kDevKvLen);
+    return;
+  }
+  if (m < 0 || m > n) {
+    if (tid == 0) atomicOr(p.err, kDevTree);
+    return;
+  }
+  const int per = m * g;   // an agent's live rows, node by node
+  const int rows = min(QM, (pooled ? p.n_agents * per : per) - QM * blk);
+  if (rows <= 0) return;
+
+  const int Nc = (int)((C + KT - 1) / KT), N = Nc + 1;
+  const int n0 = (int)((int64_t)N * split / S), NT = (int)((int64_t)N * (split + 1) / S) - n0;
+
+  if (w == 0) {
+    const bool ok = tree_masks_warp(
+        tp.parent ? tp.parent + ((int64_t)seq * tp.n_trees + tree) * n : nullptr, m, masks);
+    if (lane == 0) s_bad = !ok;
+  }
+  if (w == W0) tmem_alloc(smem_u32(tslot), T_COLS);
+  if (w == W0 + 1 && lane == 0) {
+    s_fail = 0;
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(kfull(s), 1);
+      mbar_init(kfree(s), 1);
+      mbar_init(kaready(s), 8);
+      mbar_init(ancfull(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(vfull(s), 1);
+      mbar_init(vfree(s), 1);
+      mbar_init(dkfull(s), 1);
+      mbar_init(dkfree(s), 8);
+      mbar_init(sfull(s), 1);
+      mbar_init(pfull(s), NSM);
+    }
+    mbar_init(staken, NSM);
+    mbar_init(pvdone, 1);
+    mbar_init(qready, NSM);
+    fence_mbar_init();
+    tma_prefetch(&tmK);
+    tma_prefetch(&tmV);
+    tma_prefetch(&tmL);
+  }
+  if constexpr (KEYS) {
+    // B_k^a as the dK MMA's operand: a quarter is R rows of 16 + 16 columns (a
+    // frequency's two halves), 64-byte swizzle; rows past r (r = 8) are zero
+    const __nv_bfloat16* Bk = reinterpret_cast<const __nv_bfloat16*>(p.B_k) +
+                              (int64_t)agent0 * p.r * p.n_kv * D + kvh * D;
+    for (int i = tid; i < R * D / 8; i += C_::NTHR) {
+      const int j = i / (D / 8), col = 8 * (i % (D / 8));
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (j < p.r) v = *reinterpret_cast<const uint4*>(Bk + (int64_t)j * p.n_kv * D + col);
+      const int f = col % H2;
+      sts128(bk_u + (uint32_t)(f / 16) * (R * 64) + tile_off<32, R>(j, (col / H2) * 16 + f % 16), v.x, v.y, v.z,
+             v.w);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  int fail = 0;
+
+  if (!s_bad) {
+    if (w >= W0) {
+      if constexpr (KEYS) regs_dec<32>();
+      if (w == W0 && lane == 0 && NT > 0) {
+        // ========================================================== S and P V
+        constexpr uint32_t ID_S = KEYS ? umma_idesc_f16(QM, KT, 0, 0) : umma_idesc_bf16(QM, KT, 0, 0);
+        constexpr uint32_t ID_PV = umma_idesc_bf16(QM, D, 0, 1);
+        constexpr uint32_t ID_PL = umma_idesc_bf16(QM, R, 0, 1);
+        const uint64_t dK = umma_desc(k_u, 16, 1024, 2);
+        const uint64_t dV = umma_desc(v_u, KT * 128, 1024, 2);
+        const uint64_t dLR = umma_desc(v_u + C_::KV, KT * C_::LR_ROWB, 8 * C_::LR_ROWB, C_::LR_LAYOUT);
+        auto mma_pv = [&](int i) {
+          const int vs = i % NV;
+          if (!mbar_wait(pfull(i & 1), (i >> 1) & 1)) fail = 1;
+          if (!mbar_wait(vfull(vs), (i / NV) & 1)) fail = 1;
+          tc_fence_after();
+          const uint64_t vd = umma_desc_add(dV, vs * C_::VST), ld = umma_desc_add(dLR, vs * C_::VST);
+          const uint32_t tP = tmem + C_::t_p(i & 1), acc = i > 0 ? 1u : 0u;
+#pragma unroll
+          for (int ks = 0; ks < KT / 16; ++ks)
+            umma_bf16_ts(tmem + T_O, tP + ks * 8, umma_desc_add(vd, ks * 16 * 128), ID_PV, ks > 0 ? 1u : acc);
+#pragma unroll
+          for (int ks = 0; ks < KT / 16; ++ks)
+            umma_bf16_ts(tmem + T_OL, tP + ks * 8, umma_desc_add(ld, ks * 16 * C_::LR_ROWB), ID_PL,
+                         ks > 0 ? 1u : acc);
+          umma_commit(pvdone);
+          umma_commit(vfree(vs));
+        };
+        if (!mbar_wait(qready, 0)) fail = 1;
+        int ks_ = 0, kp = 0;
+        for (int i = 0; i < NT; ++i) {
+          if (KEYS) {
+            if (!mbar_wait(kaready(ks_), kp)) fail = 1;
+            if (i > 0 && !mbar_wait(staken, (i - 1) & 1)) fail = 1;
+          } else {
+            if (!mbar_wait(kfull(ks_), kp)) fail = 1;
+          }
+          tc_fence_after();
+          const uint64_t kd = umma_desc_add(dK, ks_ * C_::KST);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_ts(tmem + C_::t_s(i & 1), tmem + T_Q + kk * 8,
+                         umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S, kk > 0);
+          umma_commit(sfull(i & 1));
+          umma_commit(kfree(ks_));
+          if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
+          if (i > 0) mma_pv(i - 1);
+        }
+        mma_pv(NT - 1);
+      } else if (w == W0 + 1 && lane == 0) {
+        // ========================================================== loads
+        auto row0 = [&](int i) {
+          return n0 + i == Nc ? (int)(C + (int64_t)tree * n) : (n0 + i) * KT;
+        };
+        const int lrv = p.r < 16 ? 0 : R;   // r = 8: one 16-wide tile holds both halves
+        auto load_k = [&](int i) {
+          const uint32_t dst = k_u + (i % NK) * C_::KST, bar = kfull(i % NK);
+          mbar_expect_tx(bar, (uint32_t)(C_::KV + (KEYS ? C_::LRT : 0)));
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b) tma_load_4d(dst + b * KT * 128, &tmK, bar, 64 * b, row0(i), kvh, seq);
+          if constexpr (KEYS) tma_load_4d(dst + C_::KV, &tmL, bar, 0, row0(i), seq, lra);
+        };
+        auto load_v = [&](int i) {
+          const uint32_t dst = v_u + (i % NV) * C_::VST, bar = vfull(i % NV);
+          mbar_expect_tx(bar, (uint32_t)C_::VST);
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b) tma_load_4d(dst + b * KT * 128, &tmV, bar, 64 * b, row0(i), kvh, seq);
+          tma_load_4d(dst + C_::KV, &tmL, bar, lrv, row0(i), seq, lra);
+        };
+        for (int i = 0; i < min(NK, NT); ++i) {
+          load_k(i);
+          if (i < NV) load_v(i);
+        }
+        // refills in the order the MMAs free the stages: S of tile i, then P V of tile i - 1
+        for (int i = 0; i < NT; ++i) {
+          if (i + NK < NT) {
+            if (!mbar_wait(kfree(i % NK), (i / NK) & 1)) fail = 1;
+            load_k(i + NK);
+          }
+          if (i > 0 && i - 1 + NV < NT) {
+            if (!mbar_wait(vfree((i - 1) % NV), ((i - 1) / NV) & 1)) fail = 1;
+            load_v(i - 1 + NV);
+          }
+        }
+      } else if (KEYS && w == W0 + 2 && lane == 0) {
+        // ========================================================== dK
+        constexpr uint32_t ID_DK = umma_idesc_bf16(KT, 32, 0, 1);
+        const uint64_t dLRk = umma_desc(k_u + C_::KV, 16, 8 * C_::LR_ROWB, C_::LR_LAYOUT);
+        const uint64_t dBk = umma_desc(bk_u, R * 64, 8 * 64, 4);
+        int ks_ = 0, kp = 0;
+        for (int i = 0; i < NT; ++i) {
+          if (!mbar_wait(kfull(ks_), kp)) fail = 1;
+          const uint64_t lr = umma_desc_add(dLRk, ks_ * C_::KST);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const int c = i * NQ + q, b = q & 1;   // NQ is even
+            if (c >= 2 && !mbar_wait(dkfree(b), ((c >> 1) - 1) & 1)) fail = 1;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < R / 16; ++ks)
+              umma_bf16(tmem + T_DK + 32 * b, umma_desc_add(lr, ks * 32),
+                        umma_desc_add(dBk, q * (R * 64) + ks * 16 * 64), ID_DK, ks > 0);
+            umma_commit(dkfull(b));
+          }
+          if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
+        }
+      } else if (KEYS && w == W0 + 3) {
+        // ========================================================== anchors s R(k0)
+        for (int i = 0; i < NT; ++i) {
+          if (i >= 3 && !mbar_wait(kaready(i % 3), (i / 3 - 1) & 1)) fail = 1;   // build(i - 3) has read its slot
+          const int64_t k0 = n0 + i == Nc ? C : (int64_t)(n0 + i) * KT;
+          for (int f = lane; f < H2; f += 32) {
+            const float2 cs = rope_cs_exact(k0, rt.theta[f]);
+            anc[(i % 3) * 64 + f] = make_float2(cs.x * p.s, cs.y * p.s);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ancfull(i % 3));
+        }
+      }
+      __syncwarp();
+      cluster_sync_all();
+      cluster_sync_all();
+    } else if (KEYS && w >= NSM) {
+      // ============================================================ K^a build
+      regs_inc<112>();
+      const int sp = w & 3, gq = lane >> 2, t4 = lane & 3;
+      const int kb = 32 * sp + 16 * ((w - NSM) >> 2);   // this warp's 16 keys (its TMEM lanes)
+      // R(j) of keys kb + gq (+ 8) as (cos, cos) and (sin, sin) f16 pairs over two
+      // adjacent frequencies
+      uint32_t RC[NQ][2][2], RS[NQ][2][2];
+      auto offsets = [&](float j0, float j1) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int f = 16 * q + 8 * u + 2 * t4;
+            const float th0 = rt.thetaf[f], th1 = rt.thetaf[f + 1];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const float j = hh ? j1 : j0;
+              const float2 a = sincos_small(j * th0), b = sincos_small(j * th1);
+              RC[q][hh][u] = h2_bits(__floats2half2_rn(a.x, b.x));
+              RS[q][hh][u] = h2_bits(__floats2half2_rn(a.y, b.y));
+            }
+          }
+      };
+      offsets((float)(kb + gq), (float)(kb + gq + 8));
+      int ks_ = 0, kp = 0;
+      for (int i = 0; i < NT; ++i) {
+        if (n0 + i == Nc) {   // the drafted tile, a split's last: offsets are the nodes' depths
+          const int j0 = kb + gq, j1 = j0 + 8;
+          offsets(j0 < m ? (float)(__popcll(masks[j0]) - 1) : 0.f,
+                  j1 < m ? (float)(__popcll(masks[j1]) - 1) : 0.f);
+        }
+        if (!mbar_wait(kfull(ks_), kp)) fail = 1;
+        if (!mbar_wait(ancfull(ks_), kp)) fail = 1;
+        const float2* an = anc + ks_ * 64;
+        // this lane's pair of K elements in a 128-byte-swizzled row: key kb + gq
+        // (+8), 16-byte chunk (2 q + u) ^ gq, word t4
+        const uint32_t rowb = k_u + ks_ * C_::KST + (uint32_t)(kb + gq) * 128 + 4 * t4;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          const int b = q & 1;
+          if (!mbar_wait(dkfull(b), ((i * NQ + q) >> 1) & 1)) fail = 1;
+          tc_fence_after();
+          uint32_t xl[8], xh[8];
+          const uint32_t tl = tmem + T_DK + 32 * b + ((uint32_t)kb << 16);
+          tmem_ld16x256_x2(xl, tl);
+          tmem_ld16x256_x2(xh, tl + 16);
+          tmem_wait_ld_regs(xl, xh);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dkfree(b));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int f = 16 * q + 8 * u + 2 * t4;
+            const float4 a = *reinterpret_cast<const float4*>(an + f);   // two adjacent (cos, sin)
+            const __half2 ac = __floats2half2_rn(a.x, a.z), as = __floats2half2_rn(a.y, a.w);
+            const __half2 nas = __hneg2(as);
+            const uint32_t c1 = (uint32_t)(((2 * q + u) ^ gq) << 4);
+            const uint32_t c2 = D == 128 ? c1 + KT * 128 : (uint32_t)(((4 + 2 * q + u) ^ gq) << 4);
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const __half2 x1 = __floats2half2_rn(__uint_as_float(xl[4 * u + 2 * hh]),
+                                                   __uint_as_float(xl[4 * u + 2 * hh + 1]));
+              const __half2 x2 = __floats2half2_rn(__uint_as_float(xh[4 * u + 2 * hh]),
+                                                   __uint_as_float(xh[4 * u + 2 * hh + 1]));
+              const __half2 c = bits_h2(RC[q][hh][u]), sn = bits_h2(RS[q][hh][u]);
+              const __half2 y1 = __hfma2(x1, c, __hneg2(__hmul2(x2, sn)));   // R(j) dK
+              const __half2 y2 = __hfma2(x2, c, __hmul2(x1, sn));
+              const uint32_t o1 = rowb + hh * 1024 + c1, o2 = rowb + hh * 1024 + c2;
+              // K_base + s R(k0) y, the base added inside the rotation's FMAs
+              const __half2 z1 = __hfma2(ac, y1, __hfma2(nas, y2, bf16x2_h2(lds32(o1))));
+              const __half2 z2 = __hfma2(ac, y2, __hfma2(as, y1, bf16x2_h2(lds32(o2))));
+              sts32(o1, h2_bits(z1));
+              sts32(o2, h2_bits(z2));
+            }
+          }
+        }
+        fence_proxy_async_smem();   // the S MMA reads K^a through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kaready(ks_));
+        if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
+      }
+      cluster_sync_all();
+      cluster_sync_all();
+    } else {
+      // ============================================================ softmax
+      if constexpr (KEYS) regs_inc<112>();
+      const int sp = w & 3, ch = w >> 2;
+      const int row = 32 * sp + lane;                // this thread's query row (TMEM lane)
+      const uint32_t tlane = (uint32_t)(32 * sp) << 16;
+      const bool live = 32 * sp < rows;              // this warp has rows
+      const int64_t q_agent = (int64_t)n * p.n_q * D;   // elements between agents' queries
+      auto locate = [&](int r_, int& node) {         // offset of row r_ of the block in q and out
+        int R_ = QM * blk + r_, ag = agent0;
+        if (pooled) {
+          ag = R_ / per;
+          R_ -= ag * per;
+        }
+        node = R_ / g;
+        return ((int64_t)seq * p.n_agents + ag) * q_agent + ((int64_t)node * p.n_q + kvh * g + R_ % g) * D;
+      };
+      uint64_t vis = 0;   // the drafted nodes this row sees
+      if (live) {
+        uint32_t qv[D / 4];   // half a row, packed
+        int node = 0;
+        const int64_t off = locate(row < rows ? row : 0, node);
+        if (row < rows) vis = masks[node];
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + off + H2 * ch);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint4 v = row < rows ? src[c] : make_uint4(0, 0, 0, 0);
+          qv[4 * c] = v.x; qv[4 * c + 1] = v.y; qv[4 * c + 2] = v.z; qv[4 * c + 3] = v.w;
+        }
+        if constexpr (KEYS) {   // fp16 beside the fp16 K^a (bf16 values convert exactly within its range)
+#pragma unroll
+          for (int c = 0; c < D / 4; ++c) qv[c] = h2_bits(bf16x2_h2(qv[c]));
+        }
+        if constexpr (D == 128) {
+          tmem_st32x32b_x32(tmem + T_Q + (D / 4) * ch + tlane, qv);
+        } else {
+          tmem_st32x32b_x16(tmem + T_Q + (D / 4) * ch + tlane, qv);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
+
+      const float sl2 = p.scale * kLog2e;
+      float m_ref = -INFINITY, lsum = 0.f;
+      for (int i = 0; i < NT; ++i) {
+        const bool drafted = n0 + i == Nc;
+        const int cnt = drafted ? m : (int)min((int64_t)KT, C - (int64_t)(n0 + i) * KT);
+        const int buf = i & 1;
+        if (!mbar_wait(sfull(buf), (i >> 1) & 1)) fail = 1;
+        tc_fence_after();
+        uint32_t sv[2][32];
+        if (live) {
+          const uint32_t ts = tmem + C_::t_s(buf) + 64 * ch + tlane;
+          tmem_ld32x32b_x32(sv[0], ts);
+          tmem_ld32x32b_x32(sv[1], ts + 32);
+          tmem_wait_ld_r32(sv[0]);
+          tmem_wait_ld_r32(sv[1]);
+        }
+        if constexpr (KEYS) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(staken);   // S may be overwritten by the next tile's MMA
+        }
+        if (cnt < KT) {
+          // rows behind the last key may hold anything: their values become zero
+          // (a weight of zero would not cover infinities)
+          if (!mbar_wait(vfull(i % NV), (i / NV) & 1)) fail = 1;
+          const uint32_t vst = v_u + (i % NV) * C_::VST;
+          constexpr int CR = D / 8 + R / 8;   // 16-byte chunks a key
+          for (int e = tid; e < (KT - cnt) * CR; e += 32 * NSM) {
+            const int t = cnt + e / CR, c = e % CR;
+            const uint32_t a = c < D / 8 ? vst + (uint32_t)(c / 8) * (KT * 128) + t * 128 + (c % 8) * 16
+                                         : vst + C_::KV + t * C_::LR_ROWB + (c - D / 8) * 16;
+            sts128(a, 0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (live) {
+          if (drafted) {
+            // 64 nodes at most: this warp's half of the keys holds all of them or none
+            const uint64_t vm = ch == 0 ? vis : 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t v32 = (uint32_t)(vm >> (32 * h));
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!((v32 >> c) & 1u)) sv[h][c] = __float_as_uint(-INFINITY);
+            }
+          } else if (cnt < KT) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (64 * ch + 32 * h + c >= cnt) sv[h][c] = __float_as_uint(-INFINITY);
+          }
+          float mr[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float mx = __uint_as_float(sv[h][0]);
+#pragma unroll
+            for (int c = 1; c < 31; c += 2) mx = max3f(mx, __uint_as_float(sv[h][c]), __uint_as_float(sv[h][c + 1]));
+            mr[h] = fmaxf(mx, __uint_as_float(sv[h][31]));
+          }
+          const float mloc = fmaxf(mr[0], mr[1]) * sl2;   // the scale is positive
+          float* xb = xch + buf * 256;
+          xb[w * 32 + lane] = mloc;
+          bar_sync(BAR_PAIR + sp, 64);
+          const float mt = fmaxf(mloc, xb[(w ^ 4) * 32 + lane]);
+          // lazy rescale: move the reference maximum only when a row's grew by > 8
+          const bool need = mt > m_ref + 8.f || (m_ref == -INFINITY && mt != -INFINITY);
+          if (__any_sync(0xffffffffu, need)) {
+            const float m_new = fmaxf(m_ref, mt);
+            const float corr = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
+            if (i > 0) {
+              if (!mbar_wait(pvdone, (i - 1) & 1)) fail = 1;   // O holds every tile before this one
+              tc_fence_after();
+              const uint32_t to = tmem + T_O + H2 * ch + tlane, tol = tmem + T_OL + tlane;
+              // this warp's half of O and of O_lr (16 columns each: group h belongs to half h & 1)
+#pragma unroll 1
+              for (int h = 0; h < H2 / 16 + R / 16; ++h) {
+                if (h >= H2 / 16 && ((h - H2 / 16) & 1) != ch) continue;
+                const uint32_t ta = h < H2 / 16 ? to + 16 * h : tol + 16 * (h - H2 / 16);
+                uint32_t ov[16];
+                tmem_ld32x32b_x16(ov, ta);
+                tmem_wait_ld_r16(ov);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * corr);
+                tmem_st32x32b_x16(ta, ov);
+              }
+              tmem_wait_st();
+            }
+            lsum *= corr;
+            m_ref = m_new;
+          }
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t scl = f2(sl2, sl2), nmu = f2(-mu, -mu);
+          uint64_t acc = f2(0.f, 0.f);
+          uint32_t pk[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const uint64_t xa2 = fma_f2(f2(__uint_as_float(sv[h][c]), __uint_as_float(sv[h][c + 1])), scl, nmu);
+              float p0, p1;
+              if ((c / 2) % kPolyEvery == 0) {
+                const float2 pp = f2_unpack(exp2_poly_f2(xa2));
+                p0 = pp.x;
+                p1 = pp.y;
+              } else {
+                const float2 xa = f2_unpack(xa2);
+                p0 = fast_exp2(xa.x);
+                p1 = fast_exp2(xa.y);
+              }
+              acc = add_f2(acc, f2(p0, p1));
+              pk[16 * h + c / 2] = pack_bf16(p0, p1);
+            }
+          const float2 accf = f2_unpack(acc);
+          lsum += accf.x + accf.y;
+          if (KEYS && i > 0) {   // P V of the last tile has read P
+            if (!mbar_wait(pvdone, (i - 1) & 1)) fail = 1;
+            tc_fence_after();
+          }
+          tmem_st32x32b_x32(tmem + C_::t_p(buf) + 32 * ch + tlane, pk);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull(buf));
+      }
+
+      // ---- this split's partial: O as 16-byte chunks, chunk c of a row at c ^ (row mod
+      // D / 4) (no bank conflicts by rows or by columns), O_lr, then m and l
+      constexpr int NCH = D / 4;
+      const uint32_t pol = k_u + C_::P_OL, pml = k_u + C_::P_ML;
+      if (NT > 0) {
+        if (!mbar_wait(pvdone, (NT - 1) & 1)) fail = 1;
+        tc_fence_after();
+        if (live) {
+#pragma unroll 1
+          for (int h = 0; h < H2 / 16; ++h) {
+            uint32_t ov[16];
+            tmem_ld32x32b_x16(ov, tmem + T_O + H2 * ch + 16 * h + tlane);
+            tmem_wait_ld_r16(ov);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              sts128(k_u + (uint32_t)row * (D * 4) + (uint32_t)(((H2 * ch + 16 * h) / 4 + c) ^ (row & (NCH - 1))) * 16,
+                     ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
+          }
+#pragma unroll 1
+          for (int h = ch; h < R / 16; h += 2) {
+            uint32_t ov[16];
+            tmem_ld32x32b_x16(ov, tmem + T_OL + 16 * h + tlane);
+            tmem_wait_ld_r16(ov);
+#pragma unroll
+            for (int c = 0; c < 16; c += 4)
+              sts128(pol + (uint32_t)(row * R + 16 * h + c) * 4, ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
+          }
+        }
+      }
+      if (live) {
+        float* lx = xch + (NT & 1) * 256;   // the exchange buffer the last tile did not use
+        lx[w * 32 + lane] = lsum;
+        bar_sync(BAR_PAIR + sp, 64);
+        if (ch == 0) {
+          sts32(pml + row * 8, __float_as_uint(m_ref));
+          sts32(pml + row * 8 + 4, __float_as_uint(lsum + lx[(w + 4) * 32 + lane]));
+        }
+      }
+      cluster_sync_all();
+      // ---- merge: this CTA's share of the rows, four rows of a warp at a time
+      const int share = (rows + S - 1) / S;
+      const int r1 = min(rows, (split + 1) * share);
+      const int c4 = lane & (NCH - 1);   // this lane's four columns
+      const int64_t ldB = (int64_t)p.n_kv * D;
+      const int lr0 = p.r < 16 ? 8 : 0;  // r = 8: the value half sits in columns 8..15
+      for (int base = split * share + w; base < r1; base += 4 * NSM) {
+        float4 acc[4];
+        float lo[4][R > 32 ? 2 : 1], inv[4];
+        int64_t off[4];
+        int ag = agent0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r_ = base + u * NSM;
+          acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int h = 0; h < (R > 32 ? 2 : 1); ++h) lo[u][h] = 0.f;
+          inv[u] = 0.f;
+          off[u] = -1;
+          if (r_ >= r1) continue;
+          int node;
+          off[u] = locate(r_, node);
+          const float mk = lane < S ? dsmem_ld(dsmem_addr(pml + 8 * r_, lane)) : -INFINITY;
+          const float lk = lane < S ? dsmem_ld(dsmem_addr(pml + 8 * r_ + 4, lane)) : 0.f;
+          float mx = mk;
+#pragma unroll
+          for (int k = kMaxSplits / 2; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+          mx = __shfl_sync(0xffffffffu, mx, 0);
+          const float wk = mk == -INFINITY ? 0.f : fast_exp2(mk - mx);
+          float lt = wk * lk;
+#pragma unroll
+          for (int k = kMaxSplits / 2; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
+          lt = __shfl_sync(0xffffffffu, lt, 0);
+          inv[u] = lt > 0.f ? 1.f / lt : 0.f;
+          for (int k = 0; k < S; ++k) {
+            const float wv = __shfl_sync(0xffffffffu, wk, k);
+            if (wv == 0.f) continue;
+            const float4 o = dsmem_ld4(
+                dsmem_addr(k_u + (uint32_t)r_ * (D * 4) + (uint32_t)(c4 ^ (r_ & (NCH - 1))) * 16, k));
+            acc[u].x = fmaf(wv, o.x, acc[u].x);
+            acc[u].y = fmaf(wv, o.y, acc[u].y);
+            acc[u].z = fmaf(wv, o.z, acc[u].z);
+            acc[u].w = fmaf(wv, o.w, acc[u].w);
+#pragma unroll
+            for (int h = 0; h < (R > 32 ? 2 : 1); ++h)
+              if (lane + 32 * h < R)
+                lo[u][h] = fmaf(wv, dsmem_ld(dsmem_addr(pol + (uint32_t)(r_ * R + lane + 32 * h) * 4, k)), lo[u][h]);
+          }
+        }
+        // O_lr B_v^a: the four rows share each B_v row (pooled rows may be of different agents)
+        float4 z[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) z[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const __nv_bfloat16* Bv = reinterpret_cast<const __nv_bfloat16*>(p.B_v) + kvh * D + 4 * c4;
+        if (!pooled) {
+          const __nv_bfloat16* B = Bv + (int64_t)ag * p.r * ldB;
+#pragma unroll 4
+          for (int j = 0; j < p.r; ++j) {
+            const uint2 bw = *reinterpret_cast<const uint2*>(B + j * ldB);
+            const float2 blo = unpack_bf16(bw.x), bhi = unpack_bf16(bw.y);
+            const int jj = lr0 + j;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float lv = __shfl_sync(0xffffffffu, R > 32 && jj >= 32 ? lo[u][R > 32 ? 1 : 0] : lo[u][0], jj & 31);
+              z[u].x = fmaf(lv, blo.x, z[u].x);
+              z[u].y = fmaf(lv, blo.y, z[u].y);
+              z[u].z = fmaf(lv, bhi.x, z[u].z);
+              z[u].w = fmaf(lv, bhi.y, z[u].w);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r_ = base + u * NSM;
+            if (r_ >= r1) continue;
+            const __nv_bfloat16* B = Bv + (int64_t)((QM * blk + r_) / per) * p.r * ldB;
+#pragma unroll 4
+            for (int j = 0; j < p.r; ++j) {
+              const uint2 bw = *reinterpret_cast<const uint2*>(B + j * ldB);
+              const float2 blo = unpack_bf16(bw.x), bhi = unpack_bf16(bw.y);
+              const int jj = lr0 + j;
+              const float lv = __shfl_sync(0xffffffffu, R > 32 && jj >= 32 ? lo[u][R > 32 ? 1 : 0] : lo[u][0], jj & 31);
+              z[u].x = fmaf(lv, blo.x, z[u].x);
+              z[u].y = fmaf(lv, blo.y, z[u].y);
+              z[u].z = fmaf(lv, bhi.x, z[u].z);
+              z[u].w = fmaf(lv, bhi.y, z[u].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (off[u] < 0 || lane >= NCH) continue;
+          const float4 o = make_float4(fmaf(p.s, z[u].x, acc[u].x) * inv[u], fmaf(p.s, z[u].y, acc[u].y) * inv[u],
+                                       fmaf(p.s, z[u].z, acc[u].z) * inv[u], fmaf(p.s, z[u].w, acc[u].w) * inv[u]);
+          if (p.out_bf16)
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + off[u] + 4 * c4) =
+                make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+          else
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + off[u] + 4 * c4) = o;
+        }
+      }
+      cluster_sync_all();   // the partials are read before any CTA of the cluster exits
+    }
+  } else if (tid == 0) {
+    atomicOr(p.err, kDevTree);
+  }
+  if (fail) s_fail = 1;
+  tc_fence_before();
+  __syncthreads();
+  if (w == W0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, T_COLS);
+  }
+  if (tid == 0 && s_fail) atomicOr(p.err, kDevPipeWait);
+}
+
+// ------------------------------------------------------------------ host
+bool tree_maps(const AttnParams& p, int D, int R, CUtensorMap* mk, CUtensorMap* mv, CUtensorMap* ml) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint32_t one[4] = {1, 1, 1, 1};
+  cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)p.L_max, (cuuint64_t)p.n_kv, (cuuint64_t)p.n_seqs};
+  cuuint64_t ks[3] = {(cuuint64_t)p.kv_tok * 2, (cuuint64_t)p.kv_head * 2, (cuuint64_t)p.kv_seq * 2};
+  cuuint32_t kb[4] = {64, (cuuint32_t)KT, 1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (enc(i ? mv : mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(i ? p.v_base : p.k_base), kd, ks, kb,
+            one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  // LR rows [2r]: boxes of R columns (LRk at column 0, LRv at column r; at r = 8
+  // one 16-wide box holds both), in [n_lr][n_seqs][L_max][2r]
+  const int64_t n_lr = p.lr_agent ? p.n_agents : 1;
+  const int64_t lr_agent_b = p.lr_agent ? p.lr_agent * 2 : p.lr_seq * 2 * p.n_seqs;
+  cuuint64_t ld[4] = {(cuuint64_t)(2 * p.r), (cuuint64_t)p.L_max, (cuuint64_t)p.n_seqs, (cuuint64_t)n_lr};
+  cuuint64_t ls[3] = {(cuuint64_t)(2 * p.r * 2), (cuuint64_t)p.lr_seq * 2, (cuuint64_t)lr_agent_b};
+  cuuint32_t lb[4] = {(cuuint32_t)R, (cuuint32_t)KT, 1, 1};
+  return enc(ml, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.lr), ld, ls, lb, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_for(R * 2), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tree_pooled(const AttnParams& p, const TreeParams& tp) {
+  // agents share keys, masks and LR rows: their rows fill the blocks together
+  return !p.B_k && tp.n_trees == 1 && !p.lr_agent;
+}
+
+int tree_blocks(const AttnParams& p, const TreeParams& tp) {
+  const int64_t rows = (int64_t)tp.nodes * p.g * (tree_pooled(p, tp) ? p.n_agents : 1);
+  return (int)((rows + QM - 1) / QM);
+}
+
+template <int D, int R, bool KEYS>
+cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t st) {
+  using C = TCfg<D, R, KEYS>;
+  AttnParams p = pin;
+  RopeTheta rt = {};
+  for (int i = 0; i < D / 2; ++i) {
+    rt.theta[i] = std::pow(p.rope_base, -2.0 * i / D);
+    rt.thetaf[i] = (float)rt.theta[i];
+  }
+  CUtensorMap mk, mv, ml;
+  if (!tree_maps(p, D, R, &mk, &mv, &ml)) return cudaErrorInvalidValue;
+  const auto kern = attn_tree_tc_kernel<D, R, KEYS>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  // resident clusters of 1..8 CTAs per device (0: not queried yet)
+  static int resident[64][kMaxSplits + 1] = {};
+  int* res = resident[dev & 63];
+  const bool pooled = tree_pooled(p, tp);
+  const int ny = tree_blocks(p, tp) * p.n_kv * (pooled ? 1 : p.n_agents);
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::NTHR);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (res[1] == 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (KEYS && fa.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;   // setmaxnreg's split assumes it
+    for (int k = kMaxSplits; k >= 1; --k) {
+      attr[0].val.clusterDim.x = (unsigned)k;
+      cfg.gridDim = dim3((unsigned)k, 1, 1);
+      int c = 0;
+      if (cudaOccupancyMaxActiveClusters(&c, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        c = 0;
+      }
+      res[k] = c > 0 ? c : (k == 1 ? 1 : -1);
+    }
+  }
+  // splits: the least waves x (tiles of a split + the tiles' worth of a CTA's
+  // start and merge)
+  const int64_t units = (int64_t)ny * p.n_seqs, tiles = (p.max_kv_len + KT - 1) / KT + 1;
+  constexpr double kFixed = 5.0;
+  int S = 1;
+  double best = 0;
+  for (int k = 1; k <= kMaxSplits; ++k) {
+    if (res[k] < 1 || (k > 1 && k > tiles)) continue;
+    const double t = (double)((units + res[k] - 1) / res[k]) * ((tiles + k - 1) / k + kFixed);
+    if (k == 1 || t < best - 1e-9) {
+      best = t;
+      S = k;
+    }
+  }
+  p.n_splits = S;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  cfg.gridDim = dim3((unsigned)S, (unsigned)ny, (unsigned)p.n_seqs);
+  e = cudaLaunchKernelEx(&cfg, kern, mk, mv, ml, p, tp, rt, (int)pooled);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D, bool KEYS>
+cudaError_t launch_tt_r(const AttnParams& p, const TreeParams& tp, cudaStream_t st) {
+  switch (p.r) {
+    case 8:
+    case 16: return launch_tt<D, 16, KEYS>(p, tp, st);
+    case 32: return launch_tt<D, 32, KEYS>(p, tp, st);
+    default: return launch_tt<D, 64, KEYS>(p, tp, st);
+  }
+}
+
+}  // namespace
+
+// bf16 caches whose rows a tensor map can count
+bool attn_tree_bf16_supported(const AttnParams& p, const TreeParams& tp) {
+  if (p.L_max >= (1ll << 31) || p.n_seqs > 65535 || p.g > 64) return false;
+  const int64_t ny = (int64_t)tree_blocks(p, tp) * p.n_kv * (tree_pooled(p, tp) ? 1 : p.n_agents);
+  return ny <= 65535;
+}
+
+cudaError_t launch_attn_tree_bf16(const AttnParams& pin, const TreeParams& tp, la_dtype out, cudaStream_t st) {
+  AttnParams p = pin;
+  p.out_bf16 = out == LA_BF16;
+  if (p.d == 128) return p.B_k ? launch_tt_r<128, true>(p, tp, st) : launch_tt_r<128, false>(p, tp, st);
+  return p.B_k ? launch_tt_r<64, true>(p, tp, st) : launch_tt_r<64, false>(p, tp, st);
+}
+
+}  // namespace la

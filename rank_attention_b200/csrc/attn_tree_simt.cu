@@ -1,6 +1,5 @@
 // Attention of drafted trees on the CUDA cores (fp32 arithmetic): fp32 inputs,
-// whose accuracy bf16 or fp16 operands cannot meet, head_dim 64, rank 8 and
-// GQA groups the tensor-core kernel (attn_tree_bf16.cu) does not take.
+// whose accuracy bf16 or fp16 operands cannot meet (bf16: attn_tree_bf16.cu).
 //
 // One CTA = one (sequence, agent, KV head), a block of up to 64 query rows
 // (tokens x the group's heads) and one split of the keys; the splits of a
@@ -48,7 +47,7 @@ struct TsCfg {
   }
 };
 
-template <typename IO, typename OUT, int D>
+template <typename OUT, int D>
 __global__ void __launch_bounds__(NTH)
     attn_tree_simt_kernel(const AttnParams p, const TreeParams tp, const __grid_constant__ RopeTheta rt) {
   constexpr int H2 = D / 2, LD = D + 4, NV = D / 64;
@@ -102,19 +101,19 @@ __global__ void __launch_bounds__(NTH)
   if (ntok <= 0) return;   // no live node in this block (the same in the whole cluster)
   const int rows = ntok * g;
 
-  const IO* kbase = reinterpret_cast<const IO*>(p.k_base) + seq * p.kv_seq + kvh * p.kv_head;
-  const IO* vbase = reinterpret_cast<const IO*>(p.v_base) + seq * p.kv_seq + kvh * p.kv_head;
-  const IO* lrp = reinterpret_cast<const IO*>(p.lr) + seq * p.lr_seq + agent * p.lr_agent;
+  const float* kbase = reinterpret_cast<const float*>(p.k_base) + seq * p.kv_seq + kvh * p.kv_head;
+  const float* vbase = reinterpret_cast<const float*>(p.v_base) + seq * p.kv_seq + kvh * p.kv_head;
+  const float* lrp = reinterpret_cast<const float*>(p.lr) + seq * p.lr_seq + agent * p.lr_agent;
   const int64_t ldB = (int64_t)p.n_kv * D;
-  const IO* Bk = p.B_k ? reinterpret_cast<const IO*>(p.B_k) + (int64_t)agent * R * ldB + kvh * D : nullptr;
-  const IO* Bv = reinterpret_cast<const IO*>(p.B_v) + (int64_t)agent * R * ldB + kvh * D;
+  const float* Bk = p.B_k ? reinterpret_cast<const float*>(p.B_k) + (int64_t)agent * R * ldB + kvh * D : nullptr;
+  const float* Bv = reinterpret_cast<const float*>(p.B_v) + (int64_t)agent * R * ldB + kvh * D;
   const int64_t qrow0 = ((int64_t)seq * p.n_agents + agent) * p.n_q_tokens + tok0;
 
   for (int i = tid; i < RB * D; i += NTH) {
     const int row = i / D, c = i % D;
     float q = 0.f;
     if (row < rows)
-      q = to_f32(reinterpret_cast<const IO*>(p.q)[((qrow0 + row / g) * p.n_q + kvh * g + row % g) * D + c]);
+      q = reinterpret_cast<const float*>(p.q)[((qrow0 + row / g) * p.n_q + kvh * g + row % g) * D + c];
     Qs[row * LD + c] = q;
   }
   for (int i = tid; i < TK * H2; i += NTH) CS[i] = rope_cs_exact(i / H2, rt.theta[i % H2]);
@@ -149,15 +148,15 @@ __global__ void __launch_bounds__(NTH)
       const int t = i / D, c = i % D;
       float kv = 0.f, vv = 0.f;
       if (t < cnt) {
-        kv = to_f32(kbase[(row0 + t) * p.kv_tok + c]);
-        vv = to_f32(vbase[(row0 + t) * p.kv_tok + c]);
+        kv = kbase[(row0 + t) * p.kv_tok + c];
+        vv = vbase[(row0 + t) * p.kv_tok + c];
       }
       Ka[t * LD + c] = kv;
       Vs[t * LD + c] = vv;
     }
     for (int i = tid; i < TK * 2 * R; i += NTH) {
       const int t = i / (2 * R), c = i % (2 * R);
-      LRs[t * LDR + c] = t < cnt ? to_f32(lrp[(row0 + t) * 2 * R + c]) : 0.f;
+      LRs[t * LDR + c] = t < cnt ? lrp[(row0 + t) * 2 * R + c] : 0.f;
     }
     if (Bk) {
       if (tid < H2) Anc[tid] = rope_cs_exact(drafted ? C : k0, rt.theta[tid]);
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(NTH)
 #pragma unroll
       for (int u = 0; u < U; ++u) x1[u] = x2[u] = 0.f;
       for (int j = 0; j < R; ++j) {
-        const float b1 = to_f32(Bk[j * ldB + i]), b2 = to_f32(Bk[j * ldB + i + H2]);
+        const float b1 = Bk[j * ldB + i], b2 = Bk[j * ldB + i + H2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float lv = LRs[(kq + G * u) * LDR + j];
@@ -326,7 +325,7 @@ __global__ void __launch_bounds__(NTH)
     for (int j = 0; j < R; ++j) {
       const float lv = __shfl_sync(0xffffffffu, j < 32 ? lo[0] : lo[1], j & 31);
 #pragma unroll
-      for (int c = 0; c < 2 * NV; ++c) z[c] = fmaf(lv, to_f32(Bv[j * ldB + lane + 32 * c]), z[c]);
+      for (int c = 0; c < 2 * NV; ++c) z[c] = fmaf(lv, Bv[j * ldB + lane + 32 * c], z[c]);
     }
     OUT* out = reinterpret_cast<OUT*>(p.out) + ((qrow0 + row / g) * p.n_q + kvh * g + row % g) * D;
 #pragma unroll
@@ -335,13 +334,13 @@ __global__ void __launch_bounds__(NTH)
   ptx::cluster_sync_all();   // the partials are read before any CTA of the cluster exits
 }
 
-template <typename IO, typename OUT, int D>
+template <typename OUT, int D>
 cudaError_t launch_ts(const AttnParams& pin, const TreeParams& tp, cudaStream_t st) {
   AttnParams p = pin;
   RopeTheta rt = {};
   for (int i = 0; i < D / 2; ++i) rt.theta[i] = std::pow(p.rope_base, -2.0 * i / D);
   const TsCfg<D> L(p.r);
-  const auto kern = attn_tree_simt_kernel<IO, OUT, D>;
+  const auto kern = attn_tree_simt_kernel<OUT, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
   if (e != cudaSuccess) return e;
   // splits: enough CTAs for two an SM, at least two tiles a split, at most the
@@ -368,9 +367,9 @@ cudaError_t launch_ts(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename IO, typename OUT>
+template <typename OUT>
 cudaError_t launch_ts_d(const AttnParams& p, const TreeParams& tp, cudaStream_t st) {
-  return p.d == 128 ? launch_ts<IO, OUT, 128>(p, tp, st) : launch_ts<IO, OUT, 64>(p, tp, st);
+  return p.d == 128 ? launch_ts<OUT, 128>(p, tp, st) : launch_ts<OUT, 64>(p, tp, st);
 }
 
 }  // namespace
@@ -381,12 +380,8 @@ bool attn_tree_simt_supported(const AttnParams& p) {
   return (int64_t)((p.n_q_tokens + QB - 1) / QB) * p.n_agents * p.n_kv <= 65535;
 }
 
-cudaError_t launch_attn_tree_simt(const AttnParams& p, const TreeParams& tp, la_dtype io, la_dtype out,
-                                  cudaStream_t st) {
-  if (io == LA_F32 && out == LA_F32) return launch_ts_d<float, float>(p, tp, st);
-  if (io == LA_F32) return launch_ts_d<float, __nv_bfloat16>(p, tp, st);
-  if (out == LA_F32) return launch_ts_d<__nv_bfloat16, float>(p, tp, st);
-  return launch_ts_d<__nv_bfloat16, __nv_bfloat16>(p, tp, st);
+cudaError_t launch_attn_tree_simt(const AttnParams& p, const TreeParams& tp, la_dtype out, cudaStream_t st) {
+  return out == LA_F32 ? launch_ts_d<float>(p, tp, st) : launch_ts_d<__nv_bfloat16>(p, tp, st);
 }
 
 }  // namespace la

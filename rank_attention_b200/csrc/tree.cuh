@@ -20,7 +20,7 @@ struct TreeParams {
   int nodes;
 };
 
-constexpr int kDevKvLen = 1, kDevTree = 8;   // bits of the device error word
+constexpr int kDevKvLen = 1, kDevPipeWait = 2, kDevTree = 8;   // bits of the device error word
 
 // One warp: every node's ancestors (itself included) as a 64-bit mask, by
 // pointer doubling over shuffles: after k rounds a node holds its nearest
