@@ -6,11 +6,11 @@
 // head), and one split of the keys; the splits of a block are a thread-block
 // cluster and merge over distributed shared memory.  Keys stream in tiles of
 // 128: the committed context, then one tile with the tree's own nodes.  Per tile
-//   dK  = LRk B_k^a                     tcgen05, in quarters of 16 frequencies
+//   dK  = LRk B_k^a                     tcgen05, 32 frequencies at a time
 //   K^a = K_base + s R(k0) R(j) dK      CUDA cores, in fp16 over K_base
 //   S   = Q K^a^T                       tcgen05, Q (fp16) read from TMEM
 //   P   = exp2(S log2e scale - m)       CUDA cores, bf16 to TMEM
-//   O  += P V_base,  O_lr += P LRv      tcgen05, P read from TMEM
+//   [O | O_lr] += P [V_base | LRv]      tcgen05, P read from TMEM
 // and once per row out = (O + s O_lr B_v^a) / l.  R(j) turns by the key's
 // offset in its tile, or by a node's depth in the drafted tile (k0 = C there).
 // Without a key delta (KEYS = false) K_base is the operand as it lies, in bf16,
@@ -18,7 +18,7 @@
 //
 // Warps: eight softmax warps (two per TMEM sub-partition, 64 keys each), eight
 // build warps (16 keys each), and one warp each to issue S and P V, to load, to
-// issue dK (its quarters ping-pong with the build), and to form the anchors
+// issue dK (a part's MMA runs while the build turns the part before), and to form the anchors
 // s R(k0) in fp64.  The running maximum is rescaled lazily (O and l corrected
 // only when a row's maximum grows by more than 2^8).
 #include <cmath>
@@ -39,25 +39,28 @@ constexpr int kMaxSplits = 8;   // the portable cluster size
 constexpr int kPolyEvery = 4;   // every 4th pair of exponentials on the FMA pipe
 constexpr int BAR_PAIR = 2;     // named barriers 2..5: the two warps of a row block
 
-// TMEM columns.  With a key delta: Q, dK (two quarters of 32), S, P, O, O_lr;
-// without: Q, S twice (P over each), O, O_lr.
-constexpr int T_Q = 0, T_DK = 64, T_P = 256, T_O = 320, T_OL = 448, T_COLS = 512;
+// TMEM columns.  With a key delta: Q, dK (64 columns: 32 frequencies), S, P, O
+// and O_lr behind it; without: Q, S twice (P over each), O and O_lr.
+constexpr int T_Q = 0, T_DK = 64, T_P = 256, T_O = 320, T_COLS = 512;
 
 template <int D, int R, bool KEYS>
 struct TCfg {
   static constexpr int NB = KEYS ? 8 : 0;                       // build warps
   static constexpr int NTHR = 32 * (NSM + NB + 4);
-  static constexpr int NQ = D / 32;                             // quarters of 16 frequencies
+  static constexpr int NH = D / 64;                             // parts of 32 frequencies
   static constexpr int LR_ROWB = R * 2;
   static constexpr uint32_t LR_LAYOUT = LR_ROWB == 128 ? 2u : (LR_ROWB == 64 ? 4u : 6u);
-  static constexpr int KV = KT * D * 2;
-  static constexpr int LRT = KT * R * 2;
-  static constexpr int KST = KV + (KEYS ? LRT : 0);             // K_base (and LRk)
-  static constexpr int VST = KV + LRT;                          // V_base and LRv
-  static constexpr int NK = 3;
+  static constexpr int KV = KT * D * 2;                         // a K or V tile
+  static constexpr int LRK = KEYS ? KT * R * 2 : 0;             // a tile's LRk columns
+  // V_base and LRv: LRv as a third 64-column group of the same swizzled layout
+  // (columns past LRv are the tensor map's zero fill), so that one MMA of N = D + R
+  // covers P V and P LRv
+  static constexpr int VST = KV + KT * 128;
+  static constexpr int NK = 3, NL = 2;
   static constexpr int NV = KEYS && D == 128 && R == 64 ? 1 : 2;   // what 227 KB leave
-  static constexpr int OFF_V = NK * KST;
-  static constexpr int OFF_BK = OFF_V + NV * VST;
+  static constexpr int OFF_V = NK * KV;
+  static constexpr int OFF_LRK = OFF_V + NV * VST;
+  static constexpr int OFF_BK = OFF_LRK + NL * LRK;
   static constexpr int OFF_MISC = OFF_BK + (KEYS ? R * D * 2 : 0);
   // misc: anchors [3][64] float2, exchange [2][8][32] float, masks [64] u64, 32 mbarriers, TMEM slot
   static constexpr int MISC = 1536 + 2048 + 512 + 256 + 16;
@@ -67,7 +70,7 @@ struct TCfg {
   static constexpr int SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
   // the partial (O, O_lr, m and l) over the drained stages
   static constexpr int P_OL = QM * D * 4, P_ML = P_OL + QM * R * 4;
-  static_assert(P_ML + QM * 8 <= OFF_BK, "the partial lies over the stages");
+  static_assert(P_ML + QM * 8 <= OFF_LRK, "the partial lies over the stages");
   static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
   // score buffers
   __host__ __device__ static constexpr int t_s(int b) { return KEYS ? 128 : 64 + 128 * b; }
@@ -89,15 +92,16 @@ __device__ __forceinline__ void regs_dec() {
 template <int D, int R, bool KEYS>
 __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const __grid_constant__ CUtensorMap tmL, const AttnParams p, const TreeParams tp,
+                        const __grid_constant__ CUtensorMap tmL, const __grid_constant__ CUtensorMap tmLk,
+                        const AttnParams p, const TreeParams tp,
                         const __grid_constant__ RopeTheta rt, const int pooled) {
   using C_ = TCfg<D, R, KEYS>;
-  constexpr int NK = C_::NK, NV = C_::NV, NQ = C_::NQ, H2 = D / 2;
+  constexpr int NK = C_::NK, NV = C_::NV, NL = C_::NL, NH = C_::NH, H2 = D / 2, T_OL = T_O + D;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  const uint32_t k_u = sb, v_u = sb + C_::OFF_V, bk_u = sb + C_::OFF_BK;
+  const uint32_t k_u = sb, v_u = sb + C_::OFF_V, lrk_u = sb + C_::OFF_LRK, bk_u = sb + C_::OFF_BK;
   unsigned char* misc = smem + C_::OFF_MISC;
   float2* anc = reinterpret_cast<float2*>(misc);
   float* xch = reinterpret_cast<float*>(misc + 1536);
@@ -112,11 +116,11 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
   auto ancfull = [&](int s) { return b0 + 72 + 8 * s; };
   auto vfull = [&](int s) { return b0 + 96 + 8 * s; };
   auto vfree = [&](int s) { return b0 + 112 + 8 * s; };
-  auto dkfull = [&](int s) { return b0 + 128 + 8 * s; };
-  auto dkfree = [&](int s) { return b0 + 144 + 8 * s; };
+  auto lrfull = [&](int s) { return b0 + 128 + 8 * s; };
+  auto lrfree = [&](int s) { return b0 + 144 + 8 * s; };
   auto sfull = [&](int s) { return b0 + 160 + 8 * s; };
   auto pfull = [&](int s) { return b0 + 176 + 8 * s; };
-  const uint32_t staken = b0 + 192, pvdone = b0 + 200, qready = b0 + 208;
+  const uint32_t staken = b0 + 192, pvdone = b0 + 200, qready = b0 + 208, dkfull = b0 + 216, dkfree = b0 + 224;
 
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   constexpr int W0 = NSM + C_::NB;   // MMA, loads, dK, anchors
@@ -166,22 +170,25 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(vfull(s), 1);
       mbar_init(vfree(s), 1);
-      mbar_init(dkfull(s), 1);
-      mbar_init(dkfree(s), 8);
+      mbar_init(lrfull(s), 1);
+      mbar_init(lrfree(s), 1);
       mbar_init(sfull(s), 1);
       mbar_init(pfull(s), NSM);
     }
     mbar_init(staken, NSM);
     mbar_init(pvdone, 1);
     mbar_init(qready, NSM);
+    mbar_init(dkfull, 1);
+    mbar_init(dkfree, 8);
     fence_mbar_init();
     tma_prefetch(&tmK);
     tma_prefetch(&tmV);
     tma_prefetch(&tmL);
+    if (KEYS) tma_prefetch(&tmLk);
   }
   if constexpr (KEYS) {
-    // B_k^a as the dK MMA's operand: a quarter is R rows of 16 + 16 columns (a
-    // frequency's two halves), 64-byte swizzle; rows past r (r = 8) are zero
+    // B_k^a as the dK MMA's operand: a part is R rows of 32 + 32 columns (a
+    // frequency's two halves), 128-byte swizzle; rows past r (r = 8) are zero
     const __nv_bfloat16* Bk = reinterpret_cast<const __nv_bfloat16*>(p.B_k) +
                               (int64_t)agent0 * p.r * p.n_kv * D + kvh * D;
     for (int i = tid; i < R * D / 8; i += C_::NTHR) {
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       uint4 v = make_uint4(0, 0, 0, 0);
       if (j < p.r) v = *reinterpret_cast<const uint4*>(Bk + (int64_t)j * p.n_kv * D + col);
       const int f = col % H2;
-      sts128(bk_u + (uint32_t)(f / 16) * (R * 64) + tile_off<32, R>(j, (col / H2) * 16 + f % 16), v.x, v.y, v.z,
+      sts128(bk_u + (uint32_t)(f / 32) * (R * 128) + tile_off<64, R>(j, (col / H2) * 32 + f % 32), v.x, v.y, v.z,
              v.w);
     }
     fence_proxy_async_smem();
@@ -203,30 +210,29 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
   if (!s_bad) {
     if (w >= W0) {
       if constexpr (KEYS) regs_dec<32>();
-      if (w == W0 && lane == 0 && NT > 0) {
+      if (w == W0 && NT > 0) {
         // ========================================================== S and P V
+        // (the whole warp walks the loop and one elected lane issues: descriptors
+        // stay in uniform registers, about 75 cycles an MMA instead of 95)
         constexpr uint32_t ID_S = KEYS ? umma_idesc_f16(QM, KT, 0, 0) : umma_idesc_bf16(QM, KT, 0, 0);
-        constexpr uint32_t ID_PV = umma_idesc_bf16(QM, D, 0, 1);
-        constexpr uint32_t ID_PL = umma_idesc_bf16(QM, R, 0, 1);
+        constexpr uint32_t ID_PV = umma_idesc_bf16(QM, D + R, 0, 1);
         const uint64_t dK = umma_desc(k_u, 16, 1024, 2);
         const uint64_t dV = umma_desc(v_u, KT * 128, 1024, 2);
-        const uint64_t dLR = umma_desc(v_u + C_::KV, KT * C_::LR_ROWB, 8 * C_::LR_ROWB, C_::LR_LAYOUT);
-        auto mma_pv = [&](int i) {
+        auto mma_pv = [&](int i) {   // O, O_lr += P [V_base | LRv]
           const int vs = i % NV;
           if (!mbar_wait(pfull(i & 1), (i >> 1) & 1)) fail = 1;
           if (!mbar_wait(vfull(vs), (i / NV) & 1)) fail = 1;
           tc_fence_after();
-          const uint64_t vd = umma_desc_add(dV, vs * C_::VST), ld = umma_desc_add(dLR, vs * C_::VST);
-          const uint32_t tP = tmem + C_::t_p(i & 1), acc = i > 0 ? 1u : 0u;
+          if (elect_one()) {
+            const uint64_t vd = umma_desc_add(dV, vs * C_::VST);
+            const uint32_t tP = tmem + C_::t_p(i & 1), acc = i > 0 ? 1u : 0u;
 #pragma unroll
-          for (int ks = 0; ks < KT / 16; ++ks)
-            umma_bf16_ts(tmem + T_O, tP + ks * 8, umma_desc_add(vd, ks * 16 * 128), ID_PV, ks > 0 ? 1u : acc);
-#pragma unroll
-          for (int ks = 0; ks < KT / 16; ++ks)
-            umma_bf16_ts(tmem + T_OL, tP + ks * 8, umma_desc_add(ld, ks * 16 * C_::LR_ROWB), ID_PL,
-                         ks > 0 ? 1u : acc);
-          umma_commit(pvdone);
-          umma_commit(vfree(vs));
+            for (int ks = 0; ks < KT / 16; ++ks)
+              umma_bf16_ts(tmem + T_O, tP + ks * 8, umma_desc_add(vd, ks * 16 * 128), ID_PV, ks > 0 ? 1u : acc);
+            umma_commit(pvdone);
+            umma_commit(vfree(vs));
+          }
+          __syncwarp();
         };
         if (!mbar_wait(qready, 0)) fail = 1;
         int ks_ = 0, kp = 0;
@@ -238,13 +244,16 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             if (!mbar_wait(kfull(ks_), kp)) fail = 1;
           }
           tc_fence_after();
-          const uint64_t kd = umma_desc_add(dK, ks_ * C_::KST);
+          if (elect_one()) {
+            const uint64_t kd = umma_desc_add(dK, ks_ * C_::KV);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_ts(tmem + C_::t_s(i & 1), tmem + T_Q + kk * 8,
-                         umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S, kk > 0);
-          umma_commit(sfull(i & 1));
-          umma_commit(kfree(ks_));
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_bf16_ts(tmem + C_::t_s(i & 1), tmem + T_Q + kk * 8,
+                           umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S, kk > 0);
+            umma_commit(sfull(i & 1));
+            umma_commit(kfree(ks_));
+          }
+          __syncwarp();
           if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
           if (i > 0) mma_pv(i - 1);
         }
@@ -256,11 +265,15 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         };
         const int lrv = p.r < 16 ? 0 : R;   // r = 8: one 16-wide tile holds both halves
         auto load_k = [&](int i) {
-          const uint32_t dst = k_u + (i % NK) * C_::KST, bar = kfull(i % NK);
-          mbar_expect_tx(bar, (uint32_t)(C_::KV + (KEYS ? C_::LRT : 0)));
+          const uint32_t dst = k_u + (i % NK) * C_::KV, bar = kfull(i % NK);
+          mbar_expect_tx(bar, (uint32_t)C_::KV);
 #pragma unroll
           for (int b = 0; b < D / 64; ++b) tma_load_4d(dst + b * KT * 128, &tmK, bar, 64 * b, row0(i), kvh, seq);
-          if constexpr (KEYS) tma_load_4d(dst + C_::KV, &tmL, bar, 0, row0(i), seq, lra);
+        };
+        auto load_lrk = [&](int i) {
+          const uint32_t bar = lrfull(i % NL);
+          mbar_expect_tx(bar, (uint32_t)C_::LRK);
+          tma_load_4d(lrk_u + (i % NL) * C_::LRK, &tmLk, bar, 0, row0(i), seq, lra);
         };
         auto load_v = [&](int i) {
           const uint32_t dst = v_u + (i % NV) * C_::VST, bar = vfull(i % NV);
@@ -270,11 +283,16 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
           tma_load_4d(dst + C_::KV, &tmL, bar, lrv, row0(i), seq, lra);
         };
         for (int i = 0; i < min(NK, NT); ++i) {
+          if (KEYS && i < NL) load_lrk(i);
           load_k(i);
           if (i < NV) load_v(i);
         }
-        // refills in the order the MMAs free the stages: S of tile i, then P V of tile i - 1
+        // refills in the order the MMAs free the stages: dK and S of tile i, then P V of tile i - 1
         for (int i = 0; i < NT; ++i) {
+          if (KEYS && i + NL < NT) {
+            if (!mbar_wait(lrfree(i % NL), (i / NL) & 1)) fail = 1;
+            load_lrk(i + NL);
+          }
           if (i + NK < NT) {
             if (!mbar_wait(kfree(i % NK), (i / NK) & 1)) fail = 1;
             load_k(i + NK);
@@ -284,27 +302,29 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             load_v(i - 1 + NV);
           }
         }
-      } else if (KEYS && w == W0 + 2 && lane == 0) {
+      } else if (KEYS && w == W0 + 2) {
         // ========================================================== dK
-        constexpr uint32_t ID_DK = umma_idesc_bf16(KT, 32, 0, 1);
-        const uint64_t dLRk = umma_desc(k_u + C_::KV, 16, 8 * C_::LR_ROWB, C_::LR_LAYOUT);
-        const uint64_t dBk = umma_desc(bk_u, R * 64, 8 * 64, 4);
-        int ks_ = 0, kp = 0;
+        constexpr uint32_t ID_DK = umma_idesc_bf16(KT, 64, 0, 1);
+        const uint64_t dLRk = umma_desc(lrk_u, 16, 8 * C_::LR_ROWB, C_::LR_LAYOUT);
+        const uint64_t dBk = umma_desc(bk_u, R * 128, 1024, 2);
         for (int i = 0; i < NT; ++i) {
-          if (!mbar_wait(kfull(ks_), kp)) fail = 1;
-          const uint64_t lr = umma_desc_add(dLRk, ks_ * C_::KST);
+          if (!mbar_wait(lrfull(i % NL), (i / NL) & 1)) fail = 1;
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const int c = i * NQ + q, b = q & 1;   // NQ is even
-            if (c >= 2 && !mbar_wait(dkfree(b), ((c >> 1) - 1) & 1)) fail = 1;
+          for (int h = 0; h < NH; ++h) {
+            const int c = i * NH + h;
+            if (c > 0 && !mbar_wait(dkfree, (c - 1) & 1)) fail = 1;
             tc_fence_after();
+            if (elect_one()) {
+              const uint64_t lr = umma_desc_add(dLRk, (i % NL) * C_::LRK);
 #pragma unroll
-            for (int ks = 0; ks < R / 16; ++ks)
-              umma_bf16(tmem + T_DK + 32 * b, umma_desc_add(lr, ks * 32),
-                        umma_desc_add(dBk, q * (R * 64) + ks * 16 * 64), ID_DK, ks > 0);
-            umma_commit(dkfull(b));
+              for (int ks = 0; ks < R / 16; ++ks)
+                umma_bf16(tmem + T_DK, umma_desc_add(lr, ks * 32),
+                          umma_desc_add(dBk, h * (R * 128) + ks * 16 * 128), ID_DK, ks > 0);
+              umma_commit(dkfull);
+              if (h == NH - 1) umma_commit(lrfree(i % NL));
+            }
+            __syncwarp();
           }
-          if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
         }
       } else if (KEYS && w == W0 + 3) {
         // ========================================================== anchors s R(k0)
@@ -329,10 +349,10 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       const int kb = 32 * sp + 16 * ((w - NSM) >> 2);   // this warp's 16 keys (its TMEM lanes)
       // R(j) of keys kb + gq (+ 8) as (cos, cos) and (sin, sin) f16 pairs over two
       // adjacent frequencies
-      uint32_t RC[NQ][2][2], RS[NQ][2][2];
+      uint32_t RC[2 * NH][2][2], RS[2 * NH][2][2];
       auto offsets = [&](float j0, float j1) {
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
+        for (int q = 0; q < 2 * NH; ++q)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int f = 16 * q + 8 * u + 2 * t4;
@@ -359,20 +379,27 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         const float2* an = anc + ks_ * 64;
         // this lane's pair of K elements in a 128-byte-swizzled row: key kb + gq
         // (+8), 16-byte chunk (2 q + u) ^ gq, word t4
-        const uint32_t rowb = k_u + ks_ * C_::KST + (uint32_t)(kb + gq) * 128 + 4 * t4;
+        const uint32_t rowb = k_u + ks_ * C_::KV + (uint32_t)(kb + gq) * 128 + 4 * t4;
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const int b = q & 1;
-          if (!mbar_wait(dkfull(b), ((i * NQ + q) >> 1) & 1)) fail = 1;
+        for (int h = 0; h < NH; ++h) {
+          if (!mbar_wait(dkfull, (i * NH + h) & 1)) fail = 1;
           tc_fence_after();
-          uint32_t xl[8], xh[8];
-          const uint32_t tl = tmem + T_DK + 32 * b + ((uint32_t)kb << 16);
-          tmem_ld16x256_x2(xl, tl);
-          tmem_ld16x256_x2(xh, tl + 16);
-          tmem_wait_ld_regs(xl, xh);
+          uint32_t xa[2][8], xb[2][8];   // 32 frequencies' two halves
+          const uint32_t tl = tmem + T_DK + ((uint32_t)kb << 16);
+          tmem_ld16x256_x2(xa[0], tl);
+          tmem_ld16x256_x2(xb[0], tl + 32);
+          tmem_ld16x256_x2(xa[1], tl + 16);
+          tmem_ld16x256_x2(xb[1], tl + 48);
+          tmem_wait_ld_regs(xa[0], xb[0]);
+          tmem_wait_ld_regs(xa[1], xb[1]);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(dkfree(b));
+          if (lane == 0) mbar_arrive(dkfree);   // the next part's MMA runs during this part's turn
+#pragma unroll
+          for (int qq = 0; qq < 2; ++qq) {
+            const int q = 2 * h + qq;
+            const uint32_t(&xl)[8] = xa[qq];
+            const uint32_t(&xh)[8] = xb[qq];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int f = 16 * q + 8 * u + 2 * t4;
@@ -397,6 +424,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
               sts32(o1, h2_bits(z1));
               sts32(o2, h2_bits(z2));
             }
+          }
           }
         }
         fence_proxy_async_smem();   // the S MMA reads K^a through the async proxy
@@ -476,12 +504,10 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
           // (a weight of zero would not cover infinities)
           if (!mbar_wait(vfull(i % NV), (i / NV) & 1)) fail = 1;
           const uint32_t vst = v_u + (i % NV) * C_::VST;
-          constexpr int CR = D / 8 + R / 8;   // 16-byte chunks a key
+          constexpr int CR = D / 8 + 8;   // 16-byte chunks a key
           for (int e = tid; e < (KT - cnt) * CR; e += 32 * NSM) {
             const int t = cnt + e / CR, c = e % CR;
-            const uint32_t a = c < D / 8 ? vst + (uint32_t)(c / 8) * (KT * 128) + t * 128 + (c % 8) * 16
-                                         : vst + C_::KV + t * C_::LR_ROWB + (c - D / 8) * 16;
-            sts128(a, 0, 0, 0, 0);
+            sts128(vst + (uint32_t)(c / 8) * (KT * 128) + t * 128 + (c % 8) * 16, 0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -734,7 +760,8 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
 }
 
 // ------------------------------------------------------------------ host
-bool tree_maps(const AttnParams& p, int D, int R, CUtensorMap* mk, CUtensorMap* mv, CUtensorMap* ml) {
+bool tree_maps(const AttnParams& p, int D, int R, CUtensorMap* mk, CUtensorMap* mv, CUtensorMap* ml,
+               CUtensorMap* mlk) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint32_t one[4] = {1, 1, 1, 1};
@@ -746,16 +773,22 @@ bool tree_maps(const AttnParams& p, int D, int R, CUtensorMap* mk, CUtensorMap* 
             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
-  // LR rows [2r]: boxes of R columns (LRk at column 0, LRv at column r; at r = 8
-  // one 16-wide box holds both), in [n_lr][n_seqs][L_max][2r]
+  // LR rows [2r] in [n_lr][n_seqs][L_max][2r]: LRv as 64-column boxes from column
+  // r (columns past 2r are filled with zeros), LRk as boxes of R columns from 0
+  // (at r = 8 both take the whole 16-wide row)
   const int64_t n_lr = p.lr_agent ? p.n_agents : 1;
   const int64_t lr_agent_b = p.lr_agent ? p.lr_agent * 2 : p.lr_seq * 2 * p.n_seqs;
   cuuint64_t ld[4] = {(cuuint64_t)(2 * p.r), (cuuint64_t)p.L_max, (cuuint64_t)p.n_seqs, (cuuint64_t)n_lr};
   cuuint64_t ls[3] = {(cuuint64_t)(2 * p.r * 2), (cuuint64_t)p.lr_seq * 2, (cuuint64_t)lr_agent_b};
-  cuuint32_t lb[4] = {(cuuint32_t)R, (cuuint32_t)KT, 1, 1};
-  return enc(ml, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.lr), ld, ls, lb, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_for(R * 2), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  for (int i = 0; i < 2; ++i) {
+    const int cols = i ? R : 64;
+    cuuint32_t lb[4] = {(cuuint32_t)cols, (cuuint32_t)KT, 1, 1};
+    if (enc(i ? mlk : ml, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.lr), ld, ls, lb, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_for(cols * 2), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
 }
 
 bool tree_pooled(const AttnParams& p, const TreeParams& tp) {
@@ -777,8 +810,8 @@ cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
     rt.theta[i] = std::pow(p.rope_base, -2.0 * i / D);
     rt.thetaf[i] = (float)rt.theta[i];
   }
-  CUtensorMap mk, mv, ml;
-  if (!tree_maps(p, D, R, &mk, &mv, &ml)) return cudaErrorInvalidValue;
+  CUtensorMap mk, mv, ml, mlk;
+  if (!tree_maps(p, D, R, &mk, &mv, &ml, &mlk)) return cudaErrorInvalidValue;
   const auto kern = attn_tree_tc_kernel<D, R, KEYS>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -833,7 +866,7 @@ cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   p.n_splits = S;
   attr[0].val.clusterDim.x = (unsigned)S;
   cfg.gridDim = dim3((unsigned)S, (unsigned)ny, (unsigned)p.n_seqs);
-  e = cudaLaunchKernelEx(&cfg, kern, mk, mv, ml, p, tp, rt, (int)pooled);
+  e = cudaLaunchKernelEx(&cfg, kern, mk, mv, ml, mlk, p, tp, rt, (int)pooled);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
