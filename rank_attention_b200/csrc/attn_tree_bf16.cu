@@ -135,27 +135,56 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
   const int tree = tp.n_trees > 1 ? agent0 : 0;
   const int lra = p.lr_agent ? agent0 : 0;
 
-  // the same values, so the same branch, in the whole cluster
+  // the same values, so the same branches, in the whole cluster
   const int64_t C = p.kv_len[seq];
   const int m = tp.tree_len ? tp.tree_len[seq * tp.n_trees + tree] : n;
-  if (C < 0 || C + (int64_t)tp.n_trees * n > p.max_kv_len) {
-    if (tid == 0) atomicOr(p.err, kDevKvLen);
-    return;
+  constexpr int NBK = KEYS ? (R * D / 8 + C_::NTHR - 1) / C_::NTHR : 0;
+  uint4 bkv[KEYS ? NBK : 1];
+  if constexpr (KEYS) {   // B_k^a's rows, read behind the lengths (rows past r, at r = 8, are zero)
+    const __nv_bfloat16* Bk = reinterpret_cast<const __nv_bfloat16*>(p.B_k) +
+                              (int64_t)agent0 * p.r * p.n_kv * D + kvh * D;
+#pragma unroll
+    for (int u = 0; u < NBK; ++u) {
+      const int i = tid + u * C_::NTHR, j = i / (D / 8);
+      bkv[u] = make_uint4(0, 0, 0, 0);
+      if (j < p.r) bkv[u] = *reinterpret_cast<const uint4*>(Bk + (int64_t)j * p.n_kv * D + 8 * (i % (D / 8)));
+    }
   }
-  if (m < 0 || m > n) {
-    if (tid == 0) atomicOr(p.err, kDevTree);
-    return;
-  }
+  const bool kv_ok = C >= 0 && C + (int64_t)tp.n_trees * n <= p.max_kv_len;
+  const bool tree_ok = m >= 0 && m <= n;
   const int per = m * g;   // an agent's live rows, node by node
   const int rows = min(QM, (pooled ? p.n_agents * per : per) - QM * blk);
-  if (rows <= 0) return;
-
+  if (!kv_ok || !tree_ok || rows <= 0) {
+    if (tid == 0 && !(kv_ok && tree_ok)) atomicOr(p.err, kv_ok ? kDevTree : kDevKvLen);
+    return;
+  }
   const int Nc = (int)((C + KT - 1) / KT), N = Nc + 1;
   const int n0 = (int)((int64_t)N * split / S), NT = (int)((int64_t)N * (split + 1) / S) - n0;
 
+  // loads: K_base, LRk and V_base with LRv of the CTA's tile i
+  auto row0 = [&](int i) { return n0 + i == Nc ? (int)(C + (int64_t)tree * n) : (n0 + i) * KT; };
+  auto load_k = [&](int i) {
+    const uint32_t dst = k_u + (i % NK) * C_::KV, bar = kfull(i % NK);
+    mbar_expect_tx(bar, (uint32_t)C_::KV);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) tma_load_4d(dst + b * KT * 128, &tmK, bar, 64 * b, row0(i), kvh, seq);
+  };
+  auto load_lrk = [&](int i) {
+    const uint32_t bar = lrfull(i % NL);
+    mbar_expect_tx(bar, (uint32_t)C_::LRK);
+    tma_load_4d(lrk_u + (i % NL) * C_::LRK, &tmLk, bar, 0, row0(i), seq, lra);
+  };
+  auto load_v = [&](int i) {
+    const uint32_t dst = v_u + (i % NV) * C_::VST, bar = vfull(i % NV);
+    mbar_expect_tx(bar, (uint32_t)C_::VST);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) tma_load_4d(dst + b * KT * 128, &tmV, bar, 64 * b, row0(i), kvh, seq);
+    tma_load_4d(dst + C_::KV, &tmL, bar, p.r < 16 ? 0 : R, row0(i), seq, lra);   // r = 8: one 16-wide row holds both
+  };
+
   if (w == 0) {
     const bool ok = tree_masks_warp(
-        tp.parent ? tp.parent + ((int64_t)seq * tp.n_trees + tree) * n : nullptr, m, masks);
+        tp.parent ? tp.parent + ((int64_t)seq * tp.n_trees + tree) * n : nullptr, n, m, masks);
     if (lane == 0) s_bad = !ok;
   }
   if (w == W0) tmem_alloc(smem_u32(tslot), T_COLS);
@@ -181,25 +210,51 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     mbar_init(dkfull, 1);
     mbar_init(dkfree, 8);
     fence_mbar_init();
-    tma_prefetch(&tmK);
-    tma_prefetch(&tmV);
-    tma_prefetch(&tmL);
-    if (KEYS) tma_prefetch(&tmLk);
+    for (int i = 0; i < min(NK, NT); ++i) {
+      if (KEYS && i < NL) load_lrk(i);
+      load_k(i);
+      if (i < NV) load_v(i);
+    }
   }
   if constexpr (KEYS) {
     // B_k^a as the dK MMA's operand: a part is R rows of 32 + 32 columns (a
-    // frequency's two halves), 128-byte swizzle; rows past r (r = 8) are zero
-    const __nv_bfloat16* Bk = reinterpret_cast<const __nv_bfloat16*>(p.B_k) +
-                              (int64_t)agent0 * p.r * p.n_kv * D + kvh * D;
-    for (int i = tid; i < R * D / 8; i += C_::NTHR) {
-      const int j = i / (D / 8), col = 8 * (i % (D / 8));
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (j < p.r) v = *reinterpret_cast<const uint4*>(Bk + (int64_t)j * p.n_kv * D + col);
-      const int f = col % H2;
-      sts128(bk_u + (uint32_t)(f / 32) * (R * 128) + tile_off<64, R>(j, (col / H2) * 32 + f % 32), v.x, v.y, v.z,
-             v.w);
+    // frequency's two halves), 128-byte swizzle
+#pragma unroll
+    for (int u = 0; u < NBK; ++u) {
+      const int i = tid + u * C_::NTHR, j = i / (D / 8), col = 8 * (i % (D / 8)), f = col % H2;
+      if (i < R * D / 8)
+        sts128(bk_u + (uint32_t)(f / 32) * (R * 128) + tile_off<64, R>(j, (col / H2) * 32 + f % 32), bkv[u].x,
+               bkv[u].y, bkv[u].z, bkv[u].w);
     }
     fence_proxy_async_smem();
+  }
+  // offset of row r_ of the block in q and out
+  const int64_t q_agent = (int64_t)n * p.n_q * D;
+  auto locate = [&](int r_, int& node, int& ag) {
+    int R_ = QM * blk + r_;
+    ag = agent0;
+    if (pooled) {
+      ag = R_ / per;
+      R_ -= ag * per;
+    }
+    node = R_ / g;
+    return ((int64_t)seq * p.n_agents + ag) * q_agent + ((int64_t)node * p.n_q + kvh * g + R_ % g) * D;
+  };
+  // softmax warps: this thread's query row (TMEM lane) and half of its columns
+  const int sp = w & 3, ch = w >> 2;
+  const int row = 32 * sp + lane;
+  const bool live = 32 * sp < rows;   // this warp has rows
+  uint32_t qv[D / 4];
+  int qnode = 0;
+  if (w < NSM && live) {
+    int ag;
+    const int64_t off = locate(row < rows ? row : 0, qnode, ag);
+    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + off + H2 * ch);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const uint4 v = row < rows ? src[c] : make_uint4(0, 0, 0, 0);
+      qv[4 * c] = v.x; qv[4 * c + 1] = v.y; qv[4 * c + 2] = v.z; qv[4 * c + 3] = v.w;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -260,33 +315,6 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         mma_pv(NT - 1);
       } else if (w == W0 + 1 && lane == 0) {
         // ========================================================== loads
-        auto row0 = [&](int i) {
-          return n0 + i == Nc ? (int)(C + (int64_t)tree * n) : (n0 + i) * KT;
-        };
-        const int lrv = p.r < 16 ? 0 : R;   // r = 8: one 16-wide tile holds both halves
-        auto load_k = [&](int i) {
-          const uint32_t dst = k_u + (i % NK) * C_::KV, bar = kfull(i % NK);
-          mbar_expect_tx(bar, (uint32_t)C_::KV);
-#pragma unroll
-          for (int b = 0; b < D / 64; ++b) tma_load_4d(dst + b * KT * 128, &tmK, bar, 64 * b, row0(i), kvh, seq);
-        };
-        auto load_lrk = [&](int i) {
-          const uint32_t bar = lrfull(i % NL);
-          mbar_expect_tx(bar, (uint32_t)C_::LRK);
-          tma_load_4d(lrk_u + (i % NL) * C_::LRK, &tmLk, bar, 0, row0(i), seq, lra);
-        };
-        auto load_v = [&](int i) {
-          const uint32_t dst = v_u + (i % NV) * C_::VST, bar = vfull(i % NV);
-          mbar_expect_tx(bar, (uint32_t)C_::VST);
-#pragma unroll
-          for (int b = 0; b < D / 64; ++b) tma_load_4d(dst + b * KT * 128, &tmV, bar, 64 * b, row0(i), kvh, seq);
-          tma_load_4d(dst + C_::KV, &tmL, bar, lrv, row0(i), seq, lra);
-        };
-        for (int i = 0; i < min(NK, NT); ++i) {
-          if (KEYS && i < NL) load_lrk(i);
-          load_k(i);
-          if (i < NV) load_v(i);
-        }
         // refills in the order the MMAs free the stages: dK and S of tile i, then P V of tile i - 1
         for (int i = 0; i < NT; ++i) {
           if (KEYS && i + NL < NT) {
@@ -342,37 +370,38 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       __syncwarp();
       cluster_sync_all();
       cluster_sync_all();
-    } else if (KEYS && w >= NSM) {
+    } else {
+      if constexpr (KEYS) regs_inc<112>();
+      if (KEYS && w >= NSM) {
       // ============================================================ K^a build
-      regs_inc<112>();
-      const int sp = w & 3, gq = lane >> 2, t4 = lane & 3;
+      const int gq = lane >> 2, t4 = lane & 3;
       const int kb = 32 * sp + 16 * ((w - NSM) >> 2);   // this warp's 16 keys (its TMEM lanes)
       // R(j) of keys kb + gq (+ 8) as (cos, cos) and (sin, sin) f16 pairs over two
       // adjacent frequencies
       uint32_t RC[2 * NH][2][2], RS[2 * NH][2][2];
-      auto offsets = [&](float j0, float j1) {
-#pragma unroll
-        for (int q = 0; q < 2 * NH; ++q)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int f = 16 * q + 8 * u + 2 * t4;
-            const float th0 = rt.thetaf[f], th1 = rt.thetaf[f + 1];
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float j = hh ? j1 : j0;
-              const float2 a = sincos_small(j * th0), b = sincos_small(j * th1);
-              RC[q][hh][u] = h2_bits(__floats2half2_rn(a.x, b.x));
-              RS[q][hh][u] = h2_bits(__floats2half2_rn(a.y, b.y));
-            }
-          }
-      };
-      offsets((float)(kb + gq), (float)(kb + gq + 8));
       int ks_ = 0, kp = 0;
       for (int i = 0; i < NT; ++i) {
-        if (n0 + i == Nc) {   // the drafted tile, a split's last: offsets are the nodes' depths
-          const int j0 = kb + gq, j1 = j0 + 8;
-          offsets(j0 < m ? (float)(__popcll(masks[j0]) - 1) : 0.f,
-                  j1 < m ? (float)(__popcll(masks[j1]) - 1) : 0.f);
+        const bool drafted = n0 + i == Nc;
+        if (i == 0 || drafted) {   // the drafted tile, a split's last: offsets are the nodes' depths
+          int j0 = kb + gq, j1 = j0 + 8;
+          if (drafted) {
+            j0 = j0 < m ? __popcll(masks[j0]) - 1 : 0;
+            j1 = j1 < m ? __popcll(masks[j1]) - 1 : 0;
+          }
+#pragma unroll
+          for (int q = 0; q < 2 * NH; ++q)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int f = 16 * q + 8 * u + 2 * t4;
+              const float th0 = rt.thetaf[f], th1 = rt.thetaf[f + 1];
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const float j = (float)(hh ? j1 : j0);
+                const float2 a = sincos_small(j * th0), b = sincos_small(j * th1);
+                RC[q][hh][u] = h2_bits(__floats2half2_rn(a.x, b.x));
+                RS[q][hh][u] = h2_bits(__floats2half2_rn(a.y, b.y));
+              }
+            }
         }
         if (!mbar_wait(kfull(ks_), kp)) fail = 1;
         if (!mbar_wait(ancfull(ks_), kp)) fail = 1;
@@ -400,31 +429,44 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             const int q = 2 * h + qq;
             const uint32_t(&xl)[8] = xa[qq];
             const uint32_t(&xh)[8] = xb[qq];
+            // the quarter's base words first, so that their latencies overlap
+            uint32_t o[2][2], w1[2][2], w2[2][2];
+            constexpr uint32_t HI = D == 128 ? KT * 128 : 0;   // columns + d/2: the next box, or 4 chunks on
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int f = 16 * q + 8 * u + 2 * t4;
-            const float4 a = *reinterpret_cast<const float4*>(an + f);   // two adjacent (cos, sin)
-            const __half2 ac = __floats2half2_rn(a.x, a.z), as = __floats2half2_rn(a.y, a.w);
-            const __half2 nas = __hneg2(as);
-            const uint32_t c1 = (uint32_t)(((2 * q + u) ^ gq) << 4);
-            const uint32_t c2 = D == 128 ? c1 + KT * 128 : (uint32_t)(((4 + 2 * q + u) ^ gq) << 4);
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const __half2 x1 = __floats2half2_rn(__uint_as_float(xl[4 * u + 2 * hh]),
-                                                   __uint_as_float(xl[4 * u + 2 * hh + 1]));
-              const __half2 x2 = __floats2half2_rn(__uint_as_float(xh[4 * u + 2 * hh]),
-                                                   __uint_as_float(xh[4 * u + 2 * hh + 1]));
-              const __half2 c = bits_h2(RC[q][hh][u]), sn = bits_h2(RS[q][hh][u]);
-              const __half2 y1 = __hfma2(x1, c, __hneg2(__hmul2(x2, sn)));   // R(j) dK
-              const __half2 y2 = __hfma2(x2, c, __hmul2(x1, sn));
-              const uint32_t o1 = rowb + hh * 1024 + c1, o2 = rowb + hh * 1024 + c2;
-              // K_base + s R(k0) y, the base added inside the rotation's FMAs
-              const __half2 z1 = __hfma2(ac, y1, __hfma2(nas, y2, bf16x2_h2(lds32(o1))));
-              const __half2 z2 = __hfma2(ac, y2, __hfma2(as, y1, bf16x2_h2(lds32(o2))));
-              sts32(o1, h2_bits(z1));
-              sts32(o2, h2_bits(z2));
+              for (int hh = 0; hh < 2; ++hh) {
+                o[u][hh] = rowb + hh * 1024 + (uint32_t)(((2 * q + u) ^ gq) << 4);
+                w1[u][hh] = lds32(o[u][hh]);
+                w2[u][hh] = lds32(D == 128 ? o[u][hh] + HI : o[u][hh] ^ 64);
+              }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int f = 16 * q + 8 * u + 2 * t4;
+              const float4 a = *reinterpret_cast<const float4*>(an + f);   // two adjacent (cos, sin)
+              const __half2 ac = __floats2half2_rn(a.x, a.z), as = __floats2half2_rn(a.y, a.w);
+              const __half2 nas = __hneg2(as);
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const __half2 x1 = __floats2half2_rn(__uint_as_float(xl[4 * u + 2 * hh]),
+                                                     __uint_as_float(xl[4 * u + 2 * hh + 1]));
+                const __half2 x2 = __floats2half2_rn(__uint_as_float(xh[4 * u + 2 * hh]),
+                                                     __uint_as_float(xh[4 * u + 2 * hh + 1]));
+                const __half2 c = bits_h2(RC[q][hh][u]), sn = bits_h2(RS[q][hh][u]);
+                const __half2 y1 = __hfma2(x1, c, __hneg2(__hmul2(x2, sn)));   // R(j) dK
+                const __half2 y2 = __hfma2(x2, c, __hmul2(x1, sn));
+                // K_base + s R(k0) y, the base added inside the rotation's FMAs
+                w1[u][hh] = h2_bits(__hfma2(ac, y1, __hfma2(nas, y2, bf16x2_h2(w1[u][hh]))));
+                w2[u][hh] = h2_bits(__hfma2(ac, y2, __hfma2(as, y1, bf16x2_h2(w2[u][hh]))));
+              }
             }
-          }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                sts32(o[u][hh], w1[u][hh]);
+                sts32(D == 128 ? o[u][hh] + HI : o[u][hh] ^ 64, w2[u][hh]);
+              }
           }
         }
         fence_proxy_async_smem();   // the S MMA reads K^a through the async proxy
@@ -432,37 +474,18 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         if (lane == 0) mbar_arrive(kaready(ks_));
         if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
       }
-      cluster_sync_all();
-      cluster_sync_all();
-    } else {
+      // B_v^a for the merge over B_k^a, which the last dK has read
+      const __nv_bfloat16* Bv = reinterpret_cast<const __nv_bfloat16*>(p.B_v) +
+                                (int64_t)agent0 * p.r * p.n_kv * D + kvh * D;
+      for (int i = tid - 32 * NSM; i < p.r * D / 8; i += 256) {
+        const uint4 v = *reinterpret_cast<const uint4*>(Bv + (int64_t)(i / (D / 8)) * p.n_kv * D + 8 * (i % (D / 8)));
+        sts128(bk_u + 16 * i, v.x, v.y, v.z, v.w);
+      }
+      } else {
       // ============================================================ softmax
-      if constexpr (KEYS) regs_inc<112>();
-      const int sp = w & 3, ch = w >> 2;
-      const int row = 32 * sp + lane;                // this thread's query row (TMEM lane)
       const uint32_t tlane = (uint32_t)(32 * sp) << 16;
-      const bool live = 32 * sp < rows;              // this warp has rows
-      const int64_t q_agent = (int64_t)n * p.n_q * D;   // elements between agents' queries
-      auto locate = [&](int r_, int& node) {         // offset of row r_ of the block in q and out
-        int R_ = QM * blk + r_, ag = agent0;
-        if (pooled) {
-          ag = R_ / per;
-          R_ -= ag * per;
-        }
-        node = R_ / g;
-        return ((int64_t)seq * p.n_agents + ag) * q_agent + ((int64_t)node * p.n_q + kvh * g + R_ % g) * D;
-      };
-      uint64_t vis = 0;   // the drafted nodes this row sees
+      const uint64_t vis = live && row < rows ? masks[qnode] : 0;   // the drafted nodes this row sees
       if (live) {
-        uint32_t qv[D / 4];   // half a row, packed
-        int node = 0;
-        const int64_t off = locate(row < rows ? row : 0, node);
-        if (row < rows) vis = masks[node];
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + off + H2 * ch);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 v = row < rows ? src[c] : make_uint4(0, 0, 0, 0);
-          qv[4 * c] = v.x; qv[4 * c + 1] = v.y; qv[4 * c + 2] = v.z; qv[4 * c + 3] = v.w;
-        }
         if constexpr (KEYS) {   // fp16 beside the fp16 K^a (bf16 values convert exactly within its range)
 #pragma unroll
           for (int c = 0; c < D / 4; ++c) qv[c] = h2_bits(bf16x2_h2(qv[c]));
@@ -578,7 +601,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             for (int c = 0; c < 32; c += 2) {
               const uint64_t xa2 = fma_f2(f2(__uint_as_float(sv[h][c]), __uint_as_float(sv[h][c + 1])), scl, nmu);
               float p0, p1;
-              if ((c / 2) % kPolyEvery == 0) {
+              if (!KEYS && (c / 2) % kPolyEvery == 0) {
                 const float2 pp = f2_unpack(exp2_poly_f2(xa2));
                 p0 = pp.x;
                 p1 = pp.y;
@@ -642,112 +665,86 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
           sts32(pml + row * 8 + 4, __float_as_uint(lsum + lx[(w + 4) * 32 + lane]));
         }
       }
+      }
       cluster_sync_all();
-      // ---- merge: this CTA's share of the rows, four rows of a warp at a time
+      // ---- merge: this CTA's share of the rows, a warp a row
+      constexpr int NCH = D / 4, NW = NSM + C_::NB, NLO = R > 32 ? 2 : 1;
+      const uint32_t pol = k_u + C_::P_OL, pml = k_u + C_::P_ML;
       const int share = (rows + S - 1) / S;
       const int r1 = min(rows, (split + 1) * share);
       const int c4 = lane & (NCH - 1);   // this lane's four columns
-      const int64_t ldB = (int64_t)p.n_kv * D;
       const int lr0 = p.r < 16 ? 8 : 0;  // r = 8: the value half sits in columns 8..15
-      for (int base = split * share + w; base < r1; base += 4 * NSM) {
-        float4 acc[4];
-        float lo[4][R > 32 ? 2 : 1], inv[4];
-        int64_t off[4];
-        int ag = agent0;
+      // (kept short: it runs once, so every instruction of it is fetched cold)
+      for (int r_ = split * share + w; r_ < r1; r_ += NW) {
+        float wk = lane < S ? dsmem_ld(dsmem_addr(pml + 8 * r_, lane)) : -INFINITY;
+        const float lk = lane < S ? dsmem_ld(dsmem_addr(pml + 8 * r_ + 4, lane)) : 0.f;
+        float mx = wk;   // the splits' weights, one a lane
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r_ = base + u * NSM;
-          acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = kMaxSplits / 2; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+        wk = wk == -INFINITY ? 0.f : fast_exp2(wk - mx);
+        float lt = wk * lk;
 #pragma unroll
-          for (int h = 0; h < (R > 32 ? 2 : 1); ++h) lo[u][h] = 0.f;
-          inv[u] = 0.f;
-          off[u] = -1;
-          if (r_ >= r1) continue;
-          int node;
-          off[u] = locate(r_, node);
-          const float mk = lane < S ? dsmem_ld(dsmem_addr(pml + 8 * r_, lane)) : -INFINITY;
-          const float lk = lane < S ? dsmem_ld(dsmem_addr(pml + 8 * r_ + 4, lane)) : 0.f;
-          float mx = mk;
-#pragma unroll
-          for (int k = kMaxSplits / 2; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-          mx = __shfl_sync(0xffffffffu, mx, 0);
-          const float wk = mk == -INFINITY ? 0.f : fast_exp2(mk - mx);
-          float lt = wk * lk;
-#pragma unroll
-          for (int k = kMaxSplits / 2; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
-          lt = __shfl_sync(0xffffffffu, lt, 0);
-          inv[u] = lt > 0.f ? 1.f / lt : 0.f;
-          for (int k = 0; k < S; ++k) {
-            const float wv = __shfl_sync(0xffffffffu, wk, k);
-            if (wv == 0.f) continue;
-            const float4 o = dsmem_ld4(
-                dsmem_addr(k_u + (uint32_t)r_ * (D * 4) + (uint32_t)(c4 ^ (r_ & (NCH - 1))) * 16, k));
-            acc[u].x = fmaf(wv, o.x, acc[u].x);
-            acc[u].y = fmaf(wv, o.y, acc[u].y);
-            acc[u].z = fmaf(wv, o.z, acc[u].z);
-            acc[u].w = fmaf(wv, o.w, acc[u].w);
-#pragma unroll
-            for (int h = 0; h < (R > 32 ? 2 : 1); ++h)
-              if (lane + 32 * h < R)
-                lo[u][h] = fmaf(wv, dsmem_ld(dsmem_addr(pol + (uint32_t)(r_ * R + lane + 32 * h) * 4, k)), lo[u][h]);
-          }
-        }
-        // O_lr B_v^a: the four rows share each B_v row (pooled rows may be of different agents)
-        float4 z[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) z[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const __nv_bfloat16* Bv = reinterpret_cast<const __nv_bfloat16*>(p.B_v) + kvh * D + 4 * c4;
-        if (!pooled) {
-          const __nv_bfloat16* B = Bv + (int64_t)ag * p.r * ldB;
+        for (int k = kMaxSplits / 2; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
+        lt = __shfl_sync(0xffffffffu, lt, 0);
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const uint32_t oa = k_u + (uint32_t)r_ * (D * 4) + (uint32_t)(c4 ^ (r_ & (NCH - 1))) * 16;
+        const uint32_t la_ = pol + (uint32_t)(r_ * R + (lane & (R - 1))) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lo[NLO] = {};
 #pragma unroll 4
-          for (int j = 0; j < p.r; ++j) {
-            const uint2 bw = *reinterpret_cast<const uint2*>(B + j * ldB);
-            const float2 blo = unpack_bf16(bw.x), bhi = unpack_bf16(bw.y);
-            const int jj = lr0 + j;
+        for (int k = 0; k < S; ++k) {
+          const float wv = __shfl_sync(0xffffffffu, wk, k);
+          float4 o = dsmem_ld4(dsmem_addr(oa, k));
+          float l[NLO];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float lv = __shfl_sync(0xffffffffu, R > 32 && jj >= 32 ? lo[u][R > 32 ? 1 : 0] : lo[u][0], jj & 31);
-              z[u].x = fmaf(lv, blo.x, z[u].x);
-              z[u].y = fmaf(lv, blo.y, z[u].y);
-              z[u].z = fmaf(lv, bhi.x, z[u].z);
-              z[u].w = fmaf(lv, bhi.y, z[u].w);
-            }
-          }
-        } else {
+          for (int h = 0; h < NLO; ++h) l[h] = dsmem_ld(dsmem_addr(la_ + 128 * h, k));
+          if (wv != 0.f) {   // a split without keys leaves nothing: its words are not read as numbers
+            acc.x = fmaf(wv, o.x, acc.x);
+            acc.y = fmaf(wv, o.y, acc.y);
+            acc.z = fmaf(wv, o.z, acc.z);
+            acc.w = fmaf(wv, o.w, acc.w);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r_ = base + u * NSM;
-            if (r_ >= r1) continue;
-            const __nv_bfloat16* B = Bv + (int64_t)((QM * blk + r_) / per) * p.r * ldB;
-#pragma unroll 4
-            for (int j = 0; j < p.r; ++j) {
-              const uint2 bw = *reinterpret_cast<const uint2*>(B + j * ldB);
-              const float2 blo = unpack_bf16(bw.x), bhi = unpack_bf16(bw.y);
-              const int jj = lr0 + j;
-              const float lv = __shfl_sync(0xffffffffu, R > 32 && jj >= 32 ? lo[u][R > 32 ? 1 : 0] : lo[u][0], jj & 31);
-              z[u].x = fmaf(lv, blo.x, z[u].x);
-              z[u].y = fmaf(lv, blo.y, z[u].y);
-              z[u].z = fmaf(lv, bhi.x, z[u].z);
-              z[u].w = fmaf(lv, bhi.y, z[u].w);
-            }
+            for (int h = 0; h < NLO; ++h) lo[h] = fmaf(wv, l[h], lo[h]);
           }
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (off[u] < 0 || lane >= NCH) continue;
-          const float4 o = make_float4(fmaf(p.s, z[u].x, acc[u].x) * inv[u], fmaf(p.s, z[u].y, acc[u].y) * inv[u],
-                                       fmaf(p.s, z[u].z, acc[u].z) * inv[u], fmaf(p.s, z[u].w, acc[u].w) * inv[u]);
-          if (p.out_bf16)
-            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + off[u] + 4 * c4) =
-                make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-          else
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + off[u] + 4 * c4) = o;
+        // O_lr B_v^a (with a key delta all rows are one agent's, its B_v in shared memory)
+        int node, ag;
+        const int64_t off = locate(r_, node, ag) + 4 * c4;
+        const int64_t ldB = KEYS ? D : (int64_t)p.n_kv * D;
+        const __nv_bfloat16* B =
+            KEYS ? reinterpret_cast<const __nv_bfloat16*>(smem + C_::OFF_BK) + 4 * c4
+                 : reinterpret_cast<const __nv_bfloat16*>(p.B_v) + (int64_t)ag * p.r * ldB + kvh * D + 4 * c4;
+        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int j = 0; j < p.r; ++j) {
+          const uint2 bw = *reinterpret_cast<const uint2*>(B + j * ldB);
+          const float2 blo = unpack_bf16(bw.x), bhi = unpack_bf16(bw.y);
+          const int jj = lr0 + j;
+          const float lv = __shfl_sync(0xffffffffu, NLO > 1 && jj >= 32 ? lo[NLO - 1] : lo[0], jj & 31);
+          z.x = fmaf(lv, blo.x, z.x);
+          z.y = fmaf(lv, blo.y, z.y);
+          z.z = fmaf(lv, bhi.x, z.z);
+          z.w = fmaf(lv, bhi.y, z.w);
         }
+        if (lane >= NCH) continue;
+        const float4 o = make_float4(fmaf(p.s, z.x, acc.x) * inv, fmaf(p.s, z.y, acc.y) * inv,
+                                     fmaf(p.s, z.z, acc.z) * inv, fmaf(p.s, z.w, acc.w) * inv);
+        if (p.out_bf16)
+          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + off) =
+              make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+        else
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + off) = o;
       }
       cluster_sync_all();   // the partials are read before any CTA of the cluster exits
     }
-  } else if (tid == 0) {
-    atomicOr(p.err, kDevTree);
+  } else {
+    if (tid == 0) atomicOr(p.err, kDevTree);
+    if (w == W0 + 1 && lane == 0)   // the first loads land before the CTA ends
+      for (int i = 0; i < min(NK, NT); ++i) {
+        if (KEYS && i < NL && !mbar_wait(lrfull(i), 0)) fail = 1;
+        if (!mbar_wait(kfull(i), 0)) fail = 1;
+        if (i < NV && !mbar_wait(vfull(i), 0)) fail = 1;
+      }
   }
   if (fail) s_fail = 1;
   tc_fence_before();

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(NTH)
   }
   if (warp == 0) {
     const bool ok = tree_masks_warp(
-        tp.parent ? tp.parent + ((int64_t)seq * tp.n_trees + tree) * tp.nodes : nullptr, m, Mk);
+        tp.parent ? tp.parent + ((int64_t)seq * tp.n_trees + tree) * tp.nodes : nullptr, tp.nodes, m, Mk);
     if (lane == 0) s_ok = ok;
   }
   __syncthreads();

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(NTH)
     if (!ready) {   // the token's (cos, sin), behind the first loads
       if (tp.parent) {
         if (tid < 32) {
-          const bool ok = tree_masks_warp(tp.parent + ((int64_t)seq * tp.n_trees + tree) * p.n_tok, m, masks);
+          const bool ok = tree_masks_warp(tp.parent + ((int64_t)seq * tp.n_trees + tree) * p.n_tok, p.n_tok, m, masks);
           if (tid == 0) s_ok = ok;
         }
         __syncthreads();

@@ -25,9 +25,10 @@ constexpr int kDevKvLen = 1, kDevPipeWait = 2, kDevTree = 8;   // bits of the de
 // One warp: every node's ancestors (itself included) as a 64-bit mask, by
 // pointer doubling over shuffles: after k rounds a node holds its nearest
 // 2^k - 1 ancestors, and six rounds cover 64 nodes.  Lane l keeps nodes l and
-// l + 32 and writes mask[node]; nodes at or past m get 0.  False (in every
-// lane) if a parent is out of range.
-__device__ __forceinline__ bool tree_masks_warp(const int32_t* parent, int m, uint64_t* mask) {
+// l + 32 of the tree's n slots (read without waiting for m) and writes
+// mask[node]; nodes at or past m get 0.  False (in every lane) if one of the m
+// parents is out of range.
+__device__ __forceinline__ bool tree_masks_warp(const int32_t* parent, int n, int m, uint64_t* mask) {
   const int lane = threadIdx.x & 31;
   int an[2];
   uint64_t mk[2];
@@ -35,10 +36,15 @@ __device__ __forceinline__ bool tree_masks_warp(const int32_t* parent, int m, ui
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int j = lane + 32 * h;
-    an[h] = -1;
+    an[h] = parent && j < n ? parent[j] : j - 1;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = lane + 32 * h;
     mk[h] = 0;
-    if (j < m) {
-      an[h] = parent ? parent[j] : j - 1;
+    if (j >= m) {
+      an[h] = -1;
+    } else {
       mk[h] = 1ull << j;
       if (an[h] < -1 || an[h] >= j) {
         bad = true;
