@@ -1,5 +1,5 @@
-// lora_grouped_delta on the CUDA cores (fp32 arithmetic): fp32 tokens, and bf16
-// shapes the tensor-core kernel (grouped_bf16.cu) does not take.
+// lora_grouped_delta: the entry point, and fp32 tokens on the CUDA cores (bf16:
+// grouped_bf16.cu).
 //
 //   out = y + s (x A_a) B_a   over the rows of every segment of agent a
 //
@@ -8,7 +8,6 @@
 // distributed shared memory, and each CTA expands its share of the output
 // columns, so the r-wide rows never reach memory and one short segment still
 // spreads over CS SMs.
-#include "bf16_common.cuh"
 #include "grouped.cuh"
 #include "la_internal.cuh"
 #include "ptx.cuh"
@@ -19,7 +18,6 @@ namespace {
 constexpr int TM = 16, NTH = 256, KC = 64;
 constexpr int CS = 4;
 
-template <typename T>
 __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p) {
   __shared__ __align__(16) float xs[TM][KC + 4];
   __shared__ __align__(16) float as[KC][64];
@@ -38,8 +36,8 @@ __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p
     return;
   }
   if (t.rows == 0) return;   // the whole cluster: the same tile
-  const T* y = reinterpret_cast<const T*>(p.y) + (int64_t)t.row0 * p.ldy;
-  T* out = reinterpret_cast<T*>(p.out) + (int64_t)t.row0 * p.ldo;
+  const float* y = reinterpret_cast<const float*>(p.y) + (int64_t)t.row0 * p.ldy;
+  float* out = reinterpret_cast<float*>(p.out) + (int64_t)t.row0 * p.ldo;
   const int ns = (p.n_out + CS - 1) / CS, c0 = rank * ns, c1 = min(p.n_out, c0 + ns);
   if (t.agent < 0) {   // no adapter: out = y
     if (p.out != p.y)
@@ -49,9 +47,9 @@ __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p
       }
     return;
   }
-  const T* x = reinterpret_cast<const T*>(p.x) + (int64_t)t.row0 * p.ldx;
-  const T* A = reinterpret_cast<const T*>(p.A) + t.agent * p.a_agent;
-  const T* B = reinterpret_cast<const T*>(p.B) + (int64_t)t.agent * R * p.n_out;
+  const float* x = reinterpret_cast<const float*>(p.x) + (int64_t)t.row0 * p.ldx;
+  const float* A = reinterpret_cast<const float*>(p.A) + t.agent * p.a_agent;
+  const float* B = reinterpret_cast<const float*>(p.B) + (int64_t)t.agent * R * p.n_out;
   // hidden share: whole KC chunks
   const int chunks = (p.hidden + KC - 1) / KC;
   const int ch0 = chunks * rank / CS, ch1 = chunks * (rank + 1) / CS;
@@ -63,11 +61,11 @@ __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p
     __syncthreads();
     for (int i = tid; i < TM * KC; i += NTH) {
       const int rr = i / KC, k = k0 + i % KC;
-      xs[rr][i % KC] = rr < t.rows && k < p.hidden ? to_f32(x[rr * p.ldx + k]) : 0.f;
+      xs[rr][i % KC] = rr < t.rows && k < p.hidden ? x[rr * p.ldx + k] : 0.f;
     }
     for (int i = tid; i < KC * R; i += NTH) {
       const int k = k0 + i / R;
-      as[i / R][i % R] = k < p.hidden ? to_f32(A[(int64_t)k * R + i % R]) : 0.f;
+      as[i / R][i % R] = k < p.hidden ? A[(int64_t)k * R + i % R] : 0.f;
     }
     __syncthreads();
 #pragma unroll 8
@@ -97,7 +95,7 @@ __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p
 #pragma unroll
     for (int i = 0; i < TM; ++i) z[i] = 0.f;
     for (int j = 0; j < R; ++j) {
-      const float b = to_f32(B[(int64_t)j * p.n_out + c]);
+      const float b = B[(int64_t)j * p.n_out + c];
 #pragma unroll
       for (int i = 0; i < TM; i += 4) {
         const float4 tv = *reinterpret_cast<const float4*>(&ts[j][i]);
@@ -109,13 +107,11 @@ __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i)
-      if (i < t.rows) out[i * p.ldo + c] = from_f32<T>(fmaf(p.s, z[i], to_f32(y[i * p.ldy + c])));
+      if (i < t.rows) out[i * p.ldo + c] = fmaf(p.s, z[i], y[i * p.ldy + c]);
   }
 }
 
-}  // namespace
-
-cudaError_t launch_grouped_simt(const GroupedParams& p, la_dtype dt, cudaStream_t st) {
+cudaError_t launch_grouped_simt(const GroupedParams& p, cudaStream_t st) {
   // every segment ends in at most one short tile
   const int64_t tiles = (int64_t)(p.n_tokens + TM - 1) / TM + p.n_segs;
   cudaLaunchConfig_t cfg = {};
@@ -129,10 +125,13 @@ cudaError_t launch_grouped_simt(const GroupedParams& p, la_dtype dt, cudaStream_
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = dt == LA_BF16 ? cudaLaunchKernelEx(&cfg, grouped_simt_kernel<__nv_bfloat16>, p)
-                                      : cudaLaunchKernelEx(&cfg, grouped_simt_kernel<float>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, grouped_simt_kernel, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
+
+}  // namespace
+
+cudaError_t launch_grouped_bf16(const GroupedParams& p, cudaStream_t st);
 
 }  // namespace la
 
@@ -170,6 +169,7 @@ extern "C" la_status lora_grouped_delta(const la_grouped_args* a, la_stream_t st
   p.s = a->lora_scale;
   p.err = error_word_ptr();
   if (!p.err) return LA_ERR_CUDA;
-  const cudaError_t e = launch_grouped_simt(p, a->dtype, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a->dtype == LA_BF16 ? launch_grouped_bf16(p, st) : launch_grouped_simt(p, st);
   return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
