@@ -803,17 +803,12 @@ cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   using C = TCfg<D, R, KEYS>;
   AttnParams p = pin;
   RopeTheta rt = {};
-  for (int i = 0; i < D / 2; ++i) {
-    rt.theta[i] = std::pow(p.rope_base, -2.0 * i / D);
-    rt.thetaf[i] = (float)rt.theta[i];
-  }
+  rope_thetas(p.rope_base, D, &rt);
   CUtensorMap mk, mv, ml, mlk;
   if (!tree_maps(p, D, R, &mk, &mv, &ml, &mlk)) return cudaErrorInvalidValue;
   const auto kern = attn_tree_tc_kernel<D, R, KEYS>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   // resident clusters of 1..8 CTAs per device (0: not queried yet)
   static int resident[64][kMaxSplits + 1] = {};
@@ -832,7 +827,8 @@ cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   cfg.numAttrs = 1;
   if (res[1] == 0) {
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kern);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
     if (KEYS && fa.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;   // setmaxnreg's split assumes it
     for (int k = kMaxSplits; k >= 1; --k) {

@@ -338,7 +338,7 @@ template <typename OUT, int D>
 cudaError_t launch_ts(const AttnParams& pin, const TreeParams& tp, cudaStream_t st) {
   AttnParams p = pin;
   RopeTheta rt = {};
-  for (int i = 0; i < D / 2; ++i) rt.theta[i] = std::pow(p.rope_base, -2.0 * i / D);
+  rope_thetas(p.rope_base, D, &rt);
   const TsCfg<D> L(p.r);
   const auto kern = attn_tree_simt_kernel<OUT, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);

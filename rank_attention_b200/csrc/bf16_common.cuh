@@ -3,6 +3,7 @@
 #pragma once
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -18,6 +19,17 @@ struct RopeTheta {
   double theta[64];
   float thetaf[64];   // the same, rounded to fp32 (small in-tile angles)
 };
+
+// theta_i = base^(-2i/d), i < d / 2, as powers of one root in extended precision
+// (one pow instead of d / 2: the host's share of a short call)
+inline void rope_thetas(double base, int d, RopeTheta* rt) {
+  const long double root = std::pow((long double)base, -2.0L / d);
+  long double t = 1.0L;
+  for (int i = 0; i < d / 2; ++i, t *= root) {
+    rt->theta[i] = (double)t;
+    rt->thetaf[i] = (float)t;
+  }
+}
 
 // (cos, sin) of t * theta, the angle formed and reduced modulo 2 pi in fp64
 __device__ __forceinline__ float2 rope_cs_exact(int64_t t, double theta) {

@@ -391,8 +391,15 @@ cudaError_t launch_gt(const GroupedParams& p, cudaStream_t st) {
   // never three CTAs an SM: their TMEM would not fit
   const int smem = max(rest + ns * C::STAGE, 80 * 1024);
   const auto kern = grouped_tc_kernel<R>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  static bool allowed[64] = {};   // per device, once
+  if (!allowed[dev & 63]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 114 * 1024);
+    if (e != cudaSuccess) return e;
+    allowed[dev & 63] = true;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)CS, (unsigned)tiles, 1);
   cfg.blockDim = dim3(GNTH);

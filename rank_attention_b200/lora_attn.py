@@ -442,6 +442,8 @@ def _on_device(device: int, stream, where: str) -> int:
     if torch.cuda.current_device() != device:
         raise ValueError(f"{where}: tensors are on cuda:{device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    if stream is None:   # without building a Stream object (about 2 us a call)
+        return torch._C._cuda_getCurrentRawStream(device)
     return _stream(stream)
 
 
