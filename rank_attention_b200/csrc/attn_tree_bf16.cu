@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ CUtensorMap tmL, const __grid_constant__ CUtensorMap tmLk,
                         const AttnParams p, const TreeParams tp,
-                        const __grid_constant__ RopeTheta rt, const int pooled) {
+                        const __grid_constant__ RopeTheta rt, const int pooled, const int fold) {
   using C_ = TCfg<D, R, KEYS>;
   constexpr int NK = C_::NK, NV = C_::NV, NL = C_::NL, NH = C_::NH, H2 = D / 2, T_OL = T_O + D;
   extern __shared__ unsigned char smem_raw[];
@@ -240,13 +240,20 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     node = R_ / g;
     return ((int64_t)seq * p.n_agents + ag) * q_agent + ((int64_t)node * p.n_q + kvh * g + R_ % g) * D;
   };
-  // softmax warps: this thread's query row (TMEM lane) and half of its columns
+  // softmax warps: this thread's query row, in TMEM lane 32 sp + lane, and its half
+  // of a tile's keys.  Folded (at most 64 rows): lanes 64.. repeat the rows and take
+  // the keys 64.. of every tile for themselves, with a maximum, a sum and outputs of
+  // their own that the merge joins like those of another split; one warp (ch = 0) a
+  // sub-partition then works on scores.  Otherwise two warps share each row's keys.
   const int sp = w & 3, ch = w >> 2;
-  const int row = 32 * sp + lane;
-  const bool live = 32 * sp < rows;   // this warp has rows
+  const int tl = 32 * sp + lane;
+  const int row = fold ? tl & 63 : tl;
+  const int kh = fold ? tl >> 6 : ch;                     // half of the keys
+  const bool has = (fold ? 32 * (sp & 1) : 32 * sp) < rows;   // these lanes have rows
+  const bool live = has && !(fold && ch == 1);            // this warp has scores to weigh
   uint32_t qv[D / 4];
   int qnode = 0;
-  if (w < NSM && live) {
+  if (w < NSM && has) {
     int ag;
     const int64_t off = locate(row < rows ? row : 0, qnode, ag);
     const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + off + H2 * ch);
@@ -484,8 +491,8 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       } else {
       // ============================================================ softmax
       const uint32_t tlane = (uint32_t)(32 * sp) << 16;
-      const uint64_t vis = live && row < rows ? masks[qnode] : 0;   // the drafted nodes this row sees
-      if (live) {
+      const uint64_t vis = has && row < rows ? masks[qnode] : 0;   // the drafted nodes this row sees
+      if (has) {
         if constexpr (KEYS) {   // fp16 beside the fp16 K^a (bf16 values convert exactly within its range)
 #pragma unroll
           for (int c = 0; c < D / 4; ++c) qv[c] = h2_bits(bf16x2_h2(qv[c]));
@@ -494,6 +501,12 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
           tmem_st32x32b_x32(tmem + T_Q + (D / 4) * ch + tlane, qv);
         } else {
           tmem_st32x32b_x16(tmem + T_Q + (D / 4) * ch + tlane, qv);
+        }
+        if (KEYS && fold && ch == 0) {   // no weights for the other half's keys
+          uint32_t z[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) z[c] = 0;
+          tmem_st32x32b_x32(tmem + T_P + 32 * (1 - kh) + tlane, z);
         }
         tmem_wait_st();
       }
@@ -511,7 +524,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         tc_fence_after();
         uint32_t sv[2][32];
         if (live) {
-          const uint32_t ts = tmem + C_::t_s(buf) + 64 * ch + tlane;
+          const uint32_t ts = tmem + C_::t_s(buf) + 64 * kh + tlane;
           tmem_ld32x32b_x32(sv[0], ts);
           tmem_ld32x32b_x32(sv[1], ts + 32);
           tmem_wait_ld_r32(sv[0]);
@@ -537,7 +550,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         if (live) {
           if (drafted) {
             // 64 nodes at most: this warp's half of the keys holds all of them or none
-            const uint64_t vm = ch == 0 ? vis : 0;
+            const uint64_t vm = kh == 0 ? vis : 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t v32 = (uint32_t)(vm >> (32 * h));
@@ -550,7 +563,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                if (64 * ch + 32 * h + c >= cnt) sv[h][c] = __float_as_uint(-INFINITY);
+                if (64 * kh + 32 * h + c >= cnt) sv[h][c] = __float_as_uint(-INFINITY);
           }
           float mr[2];
 #pragma unroll
@@ -560,25 +573,26 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             for (int c = 1; c < 31; c += 2) mx = max3f(mx, __uint_as_float(sv[h][c]), __uint_as_float(sv[h][c + 1]));
             mr[h] = fmaxf(mx, __uint_as_float(sv[h][31]));
           }
-          const float mloc = fmaxf(mr[0], mr[1]) * sl2;   // the scale is positive
-          float* xb = xch + buf * 256;
-          xb[w * 32 + lane] = mloc;
-          bar_sync(BAR_PAIR + sp, 64);
-          const float mt = fmaxf(mloc, xb[(w ^ 4) * 32 + lane]);
+          float mt = fmaxf(mr[0], mr[1]) * sl2;   // the scale is positive
+          if (!fold) {
+            float* xb = xch + buf * 256;
+            xb[w * 32 + lane] = mt;
+            bar_sync(BAR_PAIR + sp, 64);
+            mt = fmaxf(mt, xb[(w ^ 4) * 32 + lane]);
+          }
           // lazy rescale: move the reference maximum only when a row's grew by > 8
           const bool need = mt > m_ref + 8.f || (m_ref == -INFINITY && mt != -INFINITY);
           if (__any_sync(0xffffffffu, need)) {
             const float m_new = fmaxf(m_ref, mt);
             const float corr = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
             if (i > 0) {
-              if (!mbar_wait(pvdone, (i - 1) & 1)) fail = 1;   // O holds every tile before this one
+              // O holds every tile before this one (S of this tile is done, so P V of tile i - 2 is)
+              if (!mbar_wait(pvdone, (i - 1) & 1)) fail = 1;
               tc_fence_after();
-              const uint32_t to = tmem + T_O + H2 * ch + tlane, tol = tmem + T_OL + tlane;
-              // this warp's half of O and of O_lr (16 columns each: group h belongs to half h & 1)
+              // O and O_lr behind it, 16 columns at a time: this warp's half, or folded all
 #pragma unroll 1
-              for (int h = 0; h < H2 / 16 + R / 16; ++h) {
-                if (h >= H2 / 16 && ((h - H2 / 16) & 1) != ch) continue;
-                const uint32_t ta = h < H2 / 16 ? to + 16 * h : tol + 16 * (h - H2 / 16);
+              for (int h = fold ? 0 : ch; h < (D + R) / 16; h += fold ? 1 : 2) {
+                const uint32_t ta = tmem + T_O + 16 * h + tlane;
                 uint32_t ov[16];
                 tmem_ld32x32b_x16(ov, ta);
                 tmem_wait_ld_r16(ov);
@@ -619,7 +633,12 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             if (!mbar_wait(pvdone, (i - 1) & 1)) fail = 1;
             tc_fence_after();
           }
-          tmem_st32x32b_x32(tmem + C_::t_p(buf) + 32 * ch + tlane, pk);
+          tmem_st32x32b_x32(tmem + C_::t_p(buf) + 32 * kh + tlane, pk);
+          if (!KEYS && fold) {   // P lies over the scores: no weights for the other half's keys
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pk[c] = 0;
+            tmem_st32x32b_x32(tmem + C_::t_p(buf) + 32 * (1 - kh) + tlane, pk);
+          }
           tmem_wait_st();
         }
         tc_fence_before();
@@ -632,9 +651,12 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       constexpr int NCH = D / 4;
       const uint32_t pol = k_u + C_::P_OL, pml = k_u + C_::P_ML;
       if (NT > 0) {
+        // a warp that did not wait for every P V: S of the last tile is done, so P V is at
+        // tile NT - 2 or past it, and the parity of NT - 1 alone would be ambiguous
+        if (NT > 1 && !mbar_wait(pvdone, (NT - 2) & 1)) fail = 1;
         if (!mbar_wait(pvdone, (NT - 1) & 1)) fail = 1;
         tc_fence_after();
-        if (live) {
+        if (has) {
 #pragma unroll 1
           for (int h = 0; h < H2 / 16; ++h) {
             uint32_t ov[16];
@@ -642,7 +664,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             tmem_wait_ld_r16(ov);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              sts128(k_u + (uint32_t)row * (D * 4) + (uint32_t)(((H2 * ch + 16 * h) / 4 + c) ^ (row & (NCH - 1))) * 16,
+              sts128(k_u + (uint32_t)tl * (D * 4) + (uint32_t)(((H2 * ch + 16 * h) / 4 + c) ^ (tl & (NCH - 1))) * 16,
                      ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
           }
 #pragma unroll 1
@@ -652,17 +674,20 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             tmem_wait_ld_r16(ov);
 #pragma unroll
             for (int c = 0; c < 16; c += 4)
-              sts128(pol + (uint32_t)(row * R + 16 * h + c) * 4, ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
+              sts128(pol + (uint32_t)(tl * R + 16 * h + c) * 4, ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
           }
         }
       }
       if (live) {
-        float* lx = xch + (NT & 1) * 256;   // the exchange buffer the last tile did not use
-        lx[w * 32 + lane] = lsum;
-        bar_sync(BAR_PAIR + sp, 64);
+        if (!fold) {
+          float* lx = xch + (NT & 1) * 256;   // the exchange buffer the last tile did not use
+          lx[w * 32 + lane] = lsum;
+          bar_sync(BAR_PAIR + sp, 64);
+          lsum += lx[(w ^ 4) * 32 + lane];
+        }
         if (ch == 0) {
-          sts32(pml + row * 8, __float_as_uint(m_ref));
-          sts32(pml + row * 8 + 4, __float_as_uint(lsum + lx[(w + 4) * 32 + lane]));
+          sts32(pml + tl * 8, __float_as_uint(m_ref));
+          sts32(pml + tl * 8 + 4, __float_as_uint(lsum));
         }
       }
       }
@@ -675,16 +700,20 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       const int c4 = lane & (NCH - 1);   // this lane's four columns
       const int lr0 = p.r < 16 ? 8 : 0;  // r = 8: the value half sits in columns 8..15
       // (kept short: it runs once, so every instruction of it is fetched cold)
+      // partial i of a row: CTA i / F, lane row + 64 (i mod F) (F = 2 folded; 64 is a
+      // multiple of the chunk swizzle's period)
+      const int F = fold ? 2 : 1, np = S * F;
       for (int r_ = split * share + w; r_ < r1; r_ += NW) {
-        float wk = lane < S ? dsmem_ld(dsmem_addr(pml + 8 * r_, lane)) : -INFINITY;
-        const float lk = lane < S ? dsmem_ld(dsmem_addr(pml + 8 * r_ + 4, lane)) : 0.f;
-        float mx = wk;   // the splits' weights, one a lane
+        const uint32_t ml = dsmem_addr(pml + 8 * (r_ + 64 * (lane & (F - 1))), lane < np ? lane / F : 0);
+        float wk = lane < np ? dsmem_ld(ml) : -INFINITY;
+        const float lk = lane < np ? dsmem_ld(ml + 4) : 0.f;
+        float mx = wk;   // the partials' weights, one a lane
 #pragma unroll
-        for (int k = kMaxSplits / 2; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+        for (int k = kMaxSplits; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
         wk = wk == -INFINITY ? 0.f : fast_exp2(wk - mx);
         float lt = wk * lk;
 #pragma unroll
-        for (int k = kMaxSplits / 2; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
+        for (int k = kMaxSplits; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
         lt = __shfl_sync(0xffffffffu, lt, 0);
         const float inv = lt > 0.f ? 1.f / lt : 0.f;
         const uint32_t oa = k_u + (uint32_t)r_ * (D * 4) + (uint32_t)(c4 ^ (r_ & (NCH - 1))) * 16;
@@ -692,12 +721,13 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float lo[NLO] = {};
 #pragma unroll 4
-        for (int k = 0; k < S; ++k) {
+        for (int k = 0; k < np; ++k) {
           const float wv = __shfl_sync(0xffffffffu, wk, k);
-          float4 o = dsmem_ld4(dsmem_addr(oa, k));
+          const int f = k & (F - 1), kc = fold ? k >> 1 : k;
+          float4 o = dsmem_ld4(dsmem_addr(oa + f * (64 * D * 4), kc));
           float l[NLO];
 #pragma unroll
-          for (int h = 0; h < NLO; ++h) l[h] = dsmem_ld(dsmem_addr(la_ + 128 * h, k));
+          for (int h = 0; h < NLO; ++h) l[h] = dsmem_ld(dsmem_addr(la_ + f * (64 * R * 4) + 128 * h, kc));
           if (wv != 0.f) {   // a split without keys leaves nothing: its words are not read as numbers
             acc.x = fmaf(wv, o.x, acc.x);
             acc.y = fmaf(wv, o.y, acc.y);
@@ -814,6 +844,8 @@ cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   static int resident[64][kMaxSplits + 1] = {};
   int* res = resident[dev & 63];
   const bool pooled = tree_pooled(p, tp);
+  // at most 64 rows: folded
+  const int fold = (int64_t)tp.nodes * p.g * (pooled ? p.n_agents : 1) <= QM / 2;
   const int ny = tree_blocks(p, tp) * p.n_kv * (pooled ? 1 : p.n_agents);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(C::NTHR);
@@ -859,7 +891,7 @@ cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   p.n_splits = S;
   attr[0].val.clusterDim.x = (unsigned)S;
   cfg.gridDim = dim3((unsigned)S, (unsigned)ny, (unsigned)p.n_seqs);
-  e = cudaLaunchKernelEx(&cfg, kern, mk, mv, ml, mlk, p, tp, rt, (int)pooled);
+  e = cudaLaunchKernelEx(&cfg, kern, mk, mv, ml, mlk, p, tp, rt, (int)pooled, fold);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
