@@ -62,8 +62,9 @@ struct TCfg {
   static constexpr int OFF_LRK = OFF_V + NV * VST;
   static constexpr int OFF_BK = OFF_LRK + NL * LRK;
   static constexpr int OFF_MISC = OFF_BK + (KEYS ? R * D * 2 : 0);
-  // misc: anchors [3][64] float2, exchange [2][8][32] float, masks [64] u64, 32 mbarriers, TMEM slot
-  static constexpr int MISC = 1536 + 2048 + 512 + 256 + 16;
+  // misc: anchors [3][64] float2, exchange [2][8][32] float, masks [64] u64, 32 mbarriers,
+  // the TMEM slot, theta [64] float
+  static constexpr int MISC = 1536 + 2048 + 512 + 256 + 16 + 256;
   // at least more than half an SM's, so that one CTA is resident: two would wait
   // for each other's TMEM across clusters
   static constexpr int NEED = 1024 + OFF_MISC + MISC;
@@ -108,12 +109,12 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
   uint64_t* masks = reinterpret_cast<uint64_t*>(misc + 3584);
   const uint32_t b0 = smem_u32(misc + 4096);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 4096 + 256);
+  float* thf = reinterpret_cast<float*>(misc + 4096 + 272);
   __shared__ int s_bad, s_fail;
 
   auto kfull = [&](int s) { return b0 + 8 * s; };
   auto kfree = [&](int s) { return b0 + 24 + 8 * s; };
   auto kaready = [&](int s) { return b0 + 48 + 8 * s; };
-  auto ancfull = [&](int s) { return b0 + 72 + 8 * s; };
   auto vfull = [&](int s) { return b0 + 96 + 8 * s; };
   auto vfree = [&](int s) { return b0 + 112 + 8 * s; };
   auto lrfull = [&](int s) { return b0 + 128 + 8 * s; };
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
   const int tree = tp.n_trees > 1 ? agent0 : 0;
   const int lra = p.lr_agent ? agent0 : 0;
 
+  pdl_wait();   // what the kernels before wrote is read from here on
   // the same values, so the same branches, in the whole cluster
   const int64_t C = p.kv_len[seq];
   const int m = tp.tree_len ? tp.tree_len[seq * tp.n_trees + tree] : n;
@@ -188,13 +190,14 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     if (lane == 0) s_bad = !ok;
   }
   if (w == W0) tmem_alloc(smem_u32(tslot), T_COLS);
+  if (KEYS && w == W0 + 3)
+    for (int f = lane; f < H2; f += 32) thf[f] = rt.thetaf[f];
   if (w == W0 + 1 && lane == 0) {
     s_fail = 0;
     for (int s = 0; s < 3; ++s) {
-      mbar_init(kfull(s), 1);
+      mbar_init(kfull(s), KEYS ? 2 : 1);   // the loads, and with a key delta the tile's anchors
       mbar_init(kfree(s), 1);
       mbar_init(kaready(s), 8);
-      mbar_init(ancfull(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(vfull(s), 1);
@@ -363,15 +366,22 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         }
       } else if (KEYS && w == W0 + 3) {
         // ========================================================== anchors s R(k0)
+        constexpr int NF = H2 / 32;   // frequencies a lane
+        double th[NF];
+#pragma unroll
+        for (int u = 0; u < NF; ++u) th[u] = rt.theta[lane + 32 * u];
+        int ks_ = 0, kp = 1;
         for (int i = 0; i < NT; ++i) {
-          if (i >= 3 && !mbar_wait(kaready(i % 3), (i / 3 - 1) & 1)) fail = 1;   // build(i - 3) has read its slot
+          if (i >= 3 && !mbar_wait(kaready(ks_), kp)) fail = 1;   // build(i - 3) has read its slot
           const int64_t k0 = n0 + i == Nc ? C : (int64_t)(n0 + i) * KT;
-          for (int f = lane; f < H2; f += 32) {
-            const float2 cs = rope_cs_exact(k0, rt.theta[f]);
-            anc[(i % 3) * 64 + f] = make_float2(cs.x * p.s, cs.y * p.s);
+#pragma unroll
+          for (int u = 0; u < NF; ++u) {
+            const float2 cs = rope_cs_exact(k0, th[u]);
+            anc[ks_ * 64 + lane + 32 * u] = make_float2(cs.x * p.s, cs.y * p.s);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(ancfull(i % 3));
+          if (lane == 0) mbar_arrive(kfull(ks_));
+          if (++ks_ == 3) { ks_ = 0; kp ^= 1; }
         }
       }
       __syncwarp();
@@ -400,7 +410,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int f = 16 * q + 8 * u + 2 * t4;
-              const float th0 = rt.thetaf[f], th1 = rt.thetaf[f + 1];
+              const float th0 = thf[f], th1 = thf[f + 1];
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
                 const float j = (float)(hh ? j1 : j0);
@@ -411,13 +421,25 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             }
         }
         if (!mbar_wait(kfull(ks_), kp)) fail = 1;
-        if (!mbar_wait(ancfull(ks_), kp)) fail = 1;
         const float2* an = anc + ks_ * 64;
         // this lane's pair of K elements in a 128-byte-swizzled row: key kb + gq
         // (+8), 16-byte chunk (2 q + u) ^ gq, word t4
         const uint32_t rowb = k_u + ks_ * C_::KV + (uint32_t)(kb + gq) * 128 + 4 * t4;
+        constexpr uint32_t HI = KT * 128;   // columns + d/2: the next box, or (d = 64) 4 chunks on
+        auto at = [&](int q, int u, int hh) { return rowb + hh * 1024 + (uint32_t)(((2 * q + u) ^ gq) << 4); };
+        auto hi = [&](uint32_t o) { return D == 128 ? o + HI : o ^ 64; };
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
+          uint32_t w1[2][2], w2[2][2];   // a quarter's base words, read together
+          auto base = [&](int q) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                w1[u][hh] = lds32(at(q, u, hh));
+                w2[u][hh] = lds32(hi(at(q, u, hh)));
+              }
+          };
           if (!mbar_wait(dkfull, (i * NH + h) & 1)) fail = 1;
           tc_fence_after();
           uint32_t xa[2][8], xb[2][8];   // 32 frequencies' two halves
@@ -436,17 +458,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             const int q = 2 * h + qq;
             const uint32_t(&xl)[8] = xa[qq];
             const uint32_t(&xh)[8] = xb[qq];
-            // the quarter's base words first, so that their latencies overlap
-            uint32_t o[2][2], w1[2][2], w2[2][2];
-            constexpr uint32_t HI = D == 128 ? KT * 128 : 0;   // columns + d/2: the next box, or 4 chunks on
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                o[u][hh] = rowb + hh * 1024 + (uint32_t)(((2 * q + u) ^ gq) << 4);
-                w1[u][hh] = lds32(o[u][hh]);
-                w2[u][hh] = lds32(D == 128 ? o[u][hh] + HI : o[u][hh] ^ 64);
-              }
+            base(q);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int f = 16 * q + 8 * u + 2 * t4;
@@ -471,8 +483,8 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
-                sts32(o[u][hh], w1[u][hh]);
-                sts32(D == 128 ? o[u][hh] + HI : o[u][hh] ^ 64, w2[u][hh]);
+                sts32(at(q, u, hh), w1[u][hh]);
+                sts32(hi(at(q, u, hh)), w2[u][hh]);
               }
           }
         }
@@ -705,36 +717,46 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       const int F = fold ? 2 : 1, np = S * F;
       for (int r_ = split * share + w; r_ < r1; r_ += NW) {
         const uint32_t ml = dsmem_addr(pml + 8 * (r_ + 64 * (lane & (F - 1))), lane < np ? lane / F : 0);
-        float wk = lane < np ? dsmem_ld(ml) : -INFINITY;
-        const float lk = lane < np ? dsmem_ld(ml + 4) : 0.f;
-        float mx = wk;   // the partials' weights, one a lane
-#pragma unroll
-        for (int k = kMaxSplits; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        wk = wk == -INFINITY ? 0.f : fast_exp2(wk - mx);
-        float lt = wk * lk;
-#pragma unroll
-        for (int k = kMaxSplits; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
-        lt = __shfl_sync(0xffffffffu, lt, 0);
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float mk = dsmem_ld(ml), lk = dsmem_ld(ml + 4);
         const uint32_t oa = k_u + (uint32_t)r_ * (D * 4) + (uint32_t)(c4 ^ (r_ & (NCH - 1))) * 16;
         const uint32_t la_ = pol + (uint32_t)(r_ * R + (lane & (R - 1))) * 4;
+        float wk = lane < np ? mk : -INFINITY, inv = 0.f;   // the partials' weights, one a lane
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float lo[NLO] = {};
-#pragma unroll 4
-        for (int k = 0; k < np; ++k) {
-          const float wv = __shfl_sync(0xffffffffu, wk, k);
-          const int f = k & (F - 1), kc = fold ? k >> 1 : k;
-          float4 o = dsmem_ld4(dsmem_addr(oa + f * (64 * D * 4), kc));
-          float l[NLO];
+#pragma unroll 1
+        for (int k0 = 0; k0 < np; k0 += 8) {
+          float4 o[8];
+          float l[8][NLO];
 #pragma unroll
-          for (int h = 0; h < NLO; ++h) l[h] = dsmem_ld(dsmem_addr(la_ + f * (64 * R * 4) + 128 * h, kc));
-          if (wv != 0.f) {   // a split without keys leaves nothing: its words are not read as numbers
-            acc.x = fmaf(wv, o.x, acc.x);
-            acc.y = fmaf(wv, o.y, acc.y);
-            acc.z = fmaf(wv, o.z, acc.z);
-            acc.w = fmaf(wv, o.w, acc.w);
+          for (int k = 0; k < 8; ++k) {   // requested before the weights are known
+            if (k0 + k >= np) break;
+            const uint32_t f = (k0 + k) & (F - 1), kc = (k0 + k) / F;
+            o[k] = dsmem_ld4(dsmem_addr(oa + f * (64 * D * 4), kc));
 #pragma unroll
-            for (int h = 0; h < NLO; ++h) lo[h] = fmaf(wv, l[h], lo[h]);
+            for (int h = 0; h < NLO; ++h) l[k][h] = dsmem_ld(dsmem_addr(la_ + f * (64 * R * 4) + 128 * h, kc));
+          }
+          if (k0 == 0) {
+            float mx = wk;
+#pragma unroll
+            for (int k = kMaxSplits; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+            wk = wk == -INFINITY ? 0.f : fast_exp2(wk - mx);
+            float lt = wk == 0.f ? 0.f : wk * lk;
+#pragma unroll
+            for (int k = kMaxSplits; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
+            lt = __shfl_sync(0xffffffffu, lt, 0);
+            inv = lt > 0.f ? 1.f / lt : 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float wv = __shfl_sync(0xffffffffu, wk, k0 + k);
+            if (wv != 0.f) {   // a split without keys leaves nothing: its words are not read as numbers
+              acc.x = fmaf(wv, o[k].x, acc.x);
+              acc.y = fmaf(wv, o[k].y, acc.y);
+              acc.z = fmaf(wv, o[k].z, acc.z);
+              acc.w = fmaf(wv, o[k].w, acc.w);
+#pragma unroll
+              for (int h = 0; h < NLO; ++h) lo[h] = fmaf(wv, l[k][h], lo[h]);
+            }
           }
         }
         // O_lr B_v^a (with a key delta all rows are one agent's, its B_v in shared memory)
@@ -772,6 +794,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     if (w == W0 + 1 && lane == 0)   // the first loads land before the CTA ends
       for (int i = 0; i < min(NK, NT); ++i) {
         if (KEYS && i < NL && !mbar_wait(lrfull(i), 0)) fail = 1;
+        if (KEYS) mbar_arrive(kfull(i));   // in the anchors' place
         if (!mbar_wait(kfull(i), 0)) fail = 1;
         if (i < NV && !mbar_wait(vfull(i), 0)) fail = 1;
       }
@@ -851,10 +874,12 @@ cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   cfg.blockDim = dim3(C::NTHR);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (res[1] == 0) {
@@ -889,6 +914,7 @@ cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
     }
   }
   p.n_splits = S;
+  cfg.numAttrs = 2;
   attr[0].val.clusterDim.x = (unsigned)S;
   cfg.gridDim = dim3((unsigned)S, (unsigned)ny, (unsigned)p.n_seqs);
   e = cudaLaunchKernelEx(&cfg, kern, mk, mv, ml, mlk, p, tp, rt, (int)pooled, fold);
