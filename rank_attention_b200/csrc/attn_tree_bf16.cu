@@ -6,7 +6,7 @@
 // head), and one split of the keys; the splits of a block are a thread-block
 // cluster and merge over distributed shared memory.  Keys stream in tiles of
 // 128: the committed context, then one tile with the tree's own nodes.  Per tile
-//   dK  = LRk B_k^a                     tcgen05, 32 frequencies at a time
+//   dK  = LRk B_k^a                     tcgen05, half the frequencies at a time
 //   K^a = K_base + s R(k0) R(j) dK      CUDA cores, in fp16 over K_base
 //   S   = Q K^a^T                       tcgen05, Q (fp16) read from TMEM
 //   P   = exp2(S log2e scale - m)       CUDA cores, bf16 to TMEM
@@ -17,7 +17,7 @@
 // and the scores are double-buffered, P lying over the scores it came from.
 //
 // Warps: eight softmax warps (two per TMEM sub-partition, 64 keys each), eight
-// build warps (16 keys each), and one warp each to issue S and P V, to load, to
+// build warps (a thread: one key, half the frequencies), and one warp each to issue S and P V, to load, to
 // issue dK (a part's MMA runs while the build turns the part before), and to form the anchors
 // s R(k0) in fp64.  The running maximum is rescaled lazily (O and l corrected
 // only when a row's maximum grows by more than 2^8).
@@ -37,7 +37,9 @@ constexpr int QM = 128;    // query rows per CTA
 constexpr int NSM = 8;     // softmax warps
 constexpr int kMaxSplits = 8;   // the portable cluster size
 constexpr int kPolyEvery = 4;   // every 4th pair of exponentials on the FMA pipe
-constexpr int BAR_PAIR = 2;     // named barriers 2..5: the two warps of a row block
+// named barriers: set-up (every thread), build warps, and the two warps of a row
+// block (one id a sub-partition and direction)
+constexpr int BAR_SETUP = 1, BAR_BUILD = 2, BAR_AB = 4, BAR_BA = 8;
 
 // TMEM columns.  With a key delta: Q, dK (64 columns: 32 frequencies), S, P, O
 // and O_lr behind it; without: Q, S twice (P over each), O and O_lr.
@@ -47,7 +49,8 @@ template <int D, int R, bool KEYS>
 struct TCfg {
   static constexpr int NB = KEYS ? 8 : 0;                       // build warps
   static constexpr int NTHR = 32 * (NSM + NB + 4);
-  static constexpr int NH = D / 64;                             // parts of 32 frequencies
+  static constexpr int FP = D / 4;                              // frequencies of a part of dK (half of them)
+  static constexpr int NDK = 32 / FP;                           // parts that fit dK's 64 TMEM columns: 1, or 2 at d = 64
   static constexpr int LR_ROWB = R * 2;
   static constexpr uint32_t LR_LAYOUT = LR_ROWB == 128 ? 2u : (LR_ROWB == 64 ? 4u : 6u);
   static constexpr int KV = KT * D * 2;                         // a K or V tile
@@ -62,9 +65,9 @@ struct TCfg {
   static constexpr int OFF_LRK = OFF_V + NV * VST;
   static constexpr int OFF_BK = OFF_LRK + NL * LRK;
   static constexpr int OFF_MISC = OFF_BK + (KEYS ? R * D * 2 : 0);
-  // misc: anchors [3][64] float2, exchange [2][8][32] float, masks [64] u64, 32 mbarriers,
+  // misc: anchors [3][64] float2, references and sums of the rows [2][128] float, masks [64] u64, 64 mbarriers,
   // the TMEM slot, theta [64] float
-  static constexpr int MISC = 1536 + 2048 + 512 + 256 + 16 + 256;
+  static constexpr int MISC = 1536 + 1024 + 512 + 512 + 16 + 256;
   // at least more than half an SM's, so that one CTA is resident: two would wait
   // for each other's TMEM across clusters
   static constexpr int NEED = 1024 + OFF_MISC + MISC;
@@ -75,7 +78,8 @@ struct TCfg {
   static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
   // score buffers
   __host__ __device__ static constexpr int t_s(int b) { return KEYS ? 128 : 64 + 128 * b; }
-  __host__ __device__ static constexpr int t_p(int b) { return KEYS ? T_P : 64 + 128 * b; }
+  // weights of a tile's half h (64 keys, 32 columns); without a key delta over that half's scores
+  __host__ __device__ static constexpr int t_p(int b, int h) { return KEYS ? T_P + 32 * h : 64 + 128 * b + 64 * h; }
 };
 
 // the split's registers: at 640 threads a CTA launches with 96 a thread
@@ -97,31 +101,37 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
                         const AttnParams p, const TreeParams tp,
                         const __grid_constant__ RopeTheta rt, const int pooled, const int fold) {
   using C_ = TCfg<D, R, KEYS>;
-  constexpr int NK = C_::NK, NV = C_::NV, NL = C_::NL, NH = C_::NH, H2 = D / 2, T_OL = T_O + D;
+  constexpr int NK = C_::NK, NV = C_::NV, NL = C_::NL, FP = C_::FP, H2 = D / 2, T_OL = T_O + D;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const uint32_t k_u = sb, v_u = sb + C_::OFF_V, lrk_u = sb + C_::OFF_LRK, bk_u = sb + C_::OFF_BK;
   unsigned char* misc = smem + C_::OFF_MISC;
-  float2* anc = reinterpret_cast<float2*>(misc);
-  float* xch = reinterpret_cast<float*>(misc + 1536);
-  uint64_t* masks = reinterpret_cast<uint64_t*>(misc + 3584);
-  const uint32_t b0 = smem_u32(misc + 4096);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 4096 + 256);
-  float* thf = reinterpret_cast<float*>(misc + 4096 + 272);
+  uint2* anc = reinterpret_cast<uint2*>(misc);   // [3][32]: s (cos, cos) and s (sin, sin) of two frequencies at k0, f16
+  float* xref = reinterpret_cast<float*>(misc + 1536);   // a row's reference maximum, handed between its two warps
+  float* xsum = xref + QM;
+  uint64_t* masks = reinterpret_cast<uint64_t*>(misc + 2560);
+  const uint32_t b0 = smem_u32(misc + 3072);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 3584);
+  float* thf = reinterpret_cast<float*>(misc + 3600);
   __shared__ int s_bad, s_fail;
 
+  // mbarriers: K stages, V stages, LRk stages, then per half of a tile (h) and buffer
   auto kfull = [&](int s) { return b0 + 8 * s; };
   auto kfree = [&](int s) { return b0 + 24 + 8 * s; };
   auto kaready = [&](int s) { return b0 + 48 + 8 * s; };
-  auto vfull = [&](int s) { return b0 + 96 + 8 * s; };
-  auto vfree = [&](int s) { return b0 + 112 + 8 * s; };
-  auto lrfull = [&](int s) { return b0 + 128 + 8 * s; };
-  auto lrfree = [&](int s) { return b0 + 144 + 8 * s; };
-  auto sfull = [&](int s) { return b0 + 160 + 8 * s; };
-  auto pfull = [&](int s) { return b0 + 176 + 8 * s; };
-  const uint32_t staken = b0 + 192, pvdone = b0 + 200, qready = b0 + 208, dkfull = b0 + 216, dkfree = b0 + 224;
+  auto vfull = [&](int s) { return b0 + 72 + 8 * s; };
+  auto vfree = [&](int s) { return b0 + 88 + 8 * s; };
+  auto lrfull = [&](int s) { return b0 + 104 + 8 * s; };
+  auto lrfree = [&](int s) { return b0 + 120 + 8 * s; };
+  auto sfull = [&](int h, int b) { return b0 + 136 + 16 * h + 8 * b; };
+  auto pfull = [&](int h, int b) { return b0 + 168 + 16 * h + 8 * b; };
+  auto staken = [&](int h) { return b0 + 200 + 8 * h; };
+  auto pvdone = [&](int h) { return b0 + 216 + 8 * h; };
+  auto dkfull = [&](int h) { return b0 + 232 + 8 * h; };
+  auto dkfree = [&](int h) { return b0 + 248 + 8 * h; };
+  const uint32_t qready = b0 + 264, treeready = b0 + 272, alldone = b0 + 280;
 
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   constexpr int W0 = NSM + C_::NB;   // MMA, loads, dK, anchors
@@ -140,18 +150,6 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
   // the same values, so the same branches, in the whole cluster
   const int64_t C = p.kv_len[seq];
   const int m = tp.tree_len ? tp.tree_len[seq * tp.n_trees + tree] : n;
-  constexpr int NBK = KEYS ? (R * D / 8 + C_::NTHR - 1) / C_::NTHR : 0;
-  uint4 bkv[KEYS ? NBK : 1];
-  if constexpr (KEYS) {   // B_k^a's rows, read behind the lengths (rows past r, at r = 8, are zero)
-    const __nv_bfloat16* Bk = reinterpret_cast<const __nv_bfloat16*>(p.B_k) +
-                              (int64_t)agent0 * p.r * p.n_kv * D + kvh * D;
-#pragma unroll
-    for (int u = 0; u < NBK; ++u) {
-      const int i = tid + u * C_::NTHR, j = i / (D / 8);
-      bkv[u] = make_uint4(0, 0, 0, 0);
-      if (j < p.r) bkv[u] = *reinterpret_cast<const uint4*>(Bk + (int64_t)j * p.n_kv * D + 8 * (i % (D / 8)));
-    }
-  }
   const bool kv_ok = C >= 0 && C + (int64_t)tp.n_trees * n <= p.max_kv_len;
   const bool tree_ok = m >= 0 && m <= n;
   const int per = m * g;   // an agent's live rows, node by node
@@ -184,53 +182,6 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     tma_load_4d(dst + C_::KV, &tmL, bar, p.r < 16 ? 0 : R, row0(i), seq, lra);   // r = 8: one 16-wide row holds both
   };
 
-  if (w == 0) {
-    const bool ok = tree_masks_warp(
-        tp.parent ? tp.parent + ((int64_t)seq * tp.n_trees + tree) * n : nullptr, n, m, masks);
-    if (lane == 0) s_bad = !ok;
-  }
-  if (w == W0) tmem_alloc(smem_u32(tslot), T_COLS);
-  if (KEYS && w == W0 + 3)
-    for (int f = lane; f < H2; f += 32) thf[f] = rt.thetaf[f];
-  if (w == W0 + 1 && lane == 0) {
-    s_fail = 0;
-    for (int s = 0; s < 3; ++s) {
-      mbar_init(kfull(s), KEYS ? 2 : 1);   // the loads, and with a key delta the tile's anchors
-      mbar_init(kfree(s), 1);
-      mbar_init(kaready(s), 8);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(vfull(s), 1);
-      mbar_init(vfree(s), 1);
-      mbar_init(lrfull(s), 1);
-      mbar_init(lrfree(s), 1);
-      mbar_init(sfull(s), 1);
-      mbar_init(pfull(s), NSM);
-    }
-    mbar_init(staken, NSM);
-    mbar_init(pvdone, 1);
-    mbar_init(qready, NSM);
-    mbar_init(dkfull, 1);
-    mbar_init(dkfree, 8);
-    fence_mbar_init();
-    for (int i = 0; i < min(NK, NT); ++i) {
-      if (KEYS && i < NL) load_lrk(i);
-      load_k(i);
-      if (i < NV) load_v(i);
-    }
-  }
-  if constexpr (KEYS) {
-    // B_k^a as the dK MMA's operand: a part is R rows of 32 + 32 columns (a
-    // frequency's two halves), 128-byte swizzle
-#pragma unroll
-    for (int u = 0; u < NBK; ++u) {
-      const int i = tid + u * C_::NTHR, j = i / (D / 8), col = 8 * (i % (D / 8)), f = col % H2;
-      if (i < R * D / 8)
-        sts128(bk_u + (uint32_t)(f / 32) * (R * 128) + tile_off<64, R>(j, (col / H2) * 32 + f % 32), bkv[u].x,
-               bkv[u].y, bkv[u].z, bkv[u].w);
-    }
-    fence_proxy_async_smem();
-  }
   // offset of row r_ of the block in q and out
   const int64_t q_agent = (int64_t)n * p.n_q * D;
   auto locate = [&](int r_, int& node, int& ag) {
@@ -243,88 +194,155 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     node = R_ / g;
     return ((int64_t)seq * p.n_agents + ag) * q_agent + ((int64_t)node * p.n_q + kvh * g + R_ % g) * D;
   };
-  // softmax warps: this thread's query row, in TMEM lane 32 sp + lane, and its half
-  // of a tile's keys.  Folded (at most 64 rows): lanes 64.. repeat the rows and take
-  // the keys 64.. of every tile for themselves, with a maximum, a sum and outputs of
-  // their own that the merge joins like those of another split; one warp (ch = 0) a
-  // sub-partition then works on scores.  Otherwise two warps share each row's keys.
-  const int sp = w & 3, ch = w >> 2;
-  const int tl = 32 * sp + lane;
-  const int row = fold ? tl & 63 : tl;
-  const int kh = fold ? tl >> 6 : ch;                     // half of the keys
-  const bool has = (fold ? 32 * (sp & 1) : 32 * sp) < rows;   // these lanes have rows
-  const bool live = has && !(fold && ch == 1);            // this warp has scores to weigh
-  uint32_t qv[D / 4];
-  int qnode = 0;
-  if (w < NSM && has) {
-    int ag;
-    const int64_t off = locate(row < rows ? row : 0, qnode, ag);
-    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + off + H2 * ch);
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      const uint4 v = row < rows ? src[c] : make_uint4(0, 0, 0, 0);
-      qv[4 * c] = v.x; qv[4 * c + 1] = v.y; qv[4 * c + 2] = v.z; qv[4 * c + 3] = v.w;
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
+  uint32_t tmem = 0;
+  auto setup_sync = [&]() {   // barriers, TMEM, queries' and B_k's first reads: each role does its share before
+    tc_fence_before();
+    bar_sync(BAR_SETUP, C_::NTHR);
+    tc_fence_after();
+    tmem = *tslot;
+  };
   int fail = 0;
 
-  if (!s_bad) {
-    if (w >= W0) {
+  if (w >= W0) {
       if constexpr (KEYS) regs_dec<32>();
-      if (w == W0 && NT > 0) {
+      if (w == W0) {
         // ========================================================== S and P V
         // (the whole warp walks the loop and one elected lane issues: descriptors
         // stay in uniform registers, about 75 cycles an MMA instead of 95)
-        constexpr uint32_t ID_S = KEYS ? umma_idesc_f16(QM, KT, 0, 0) : umma_idesc_bf16(QM, KT, 0, 0);
+        constexpr uint32_t ID_S = KEYS ? umma_idesc_f16(QM, KT / 2, 0, 0) : umma_idesc_bf16(QM, KT / 2, 0, 0);
         constexpr uint32_t ID_PV = umma_idesc_bf16(QM, D + R, 0, 1);
+        tmem_alloc(smem_u32(tslot), T_COLS);
+        setup_sync();
         const uint64_t dK = umma_desc(k_u, 16, 1024, 2);
         const uint64_t dV = umma_desc(v_u, KT * 128, 1024, 2);
-        auto mma_pv = [&](int i) {   // O, O_lr += P [V_base | LRv]
+        auto mma_pv = [&](int i, int h) {   // O, O_lr += P [V_base | LRv] over half h of tile i
           const int vs = i % NV;
-          if (!mbar_wait(pfull(i & 1), (i >> 1) & 1)) fail = 1;
-          if (!mbar_wait(vfull(vs), (i / NV) & 1)) fail = 1;
+          if (!mbar_wait(pfull(h, i & 1), (i >> 1) & 1)) fail = 1;
+          if (h == 0 && !mbar_wait(vfull(vs), (i / NV) & 1)) fail = 1;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t vd = umma_desc_add(dV, vs * C_::VST);
-            const uint32_t tP = tmem + C_::t_p(i & 1), acc = i > 0 ? 1u : 0u;
+            const uint64_t vd = umma_desc_add(dV, vs * C_::VST + h * (KT / 2) * 128);
+            const uint32_t tP = tmem + C_::t_p(i & 1, h), acc = i > 0 || h > 0 ? 1u : 0u;
 #pragma unroll
-            for (int ks = 0; ks < KT / 16; ++ks)
+            for (int ks = 0; ks < KT / 32; ++ks)
               umma_bf16_ts(tmem + T_O, tP + ks * 8, umma_desc_add(vd, ks * 16 * 128), ID_PV, ks > 0 ? 1u : acc);
-            umma_commit(pvdone);
-            umma_commit(vfree(vs));
+            umma_commit(pvdone(h));
+            if (h == 1) umma_commit(vfree(vs));
           }
           __syncwarp();
         };
-        if (!mbar_wait(qready, 0)) fail = 1;
+        if (NT > 0 && !mbar_wait(qready, 0)) fail = 1;
         int ks_ = 0, kp = 0;
-        for (int i = 0; i < NT; ++i) {
-          if (KEYS) {
-            if (!mbar_wait(kaready(ks_), kp)) fail = 1;
-            if (i > 0 && !mbar_wait(staken, (i - 1) & 1)) fail = 1;
-          } else {
-            if (!mbar_wait(kfull(ks_), kp)) fail = 1;
-          }
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t kd = umma_desc_add(dK, ks_ * C_::KV);
+        if (fold) {
+          // whole tiles: S of 128 keys, and P V once a row's both halves have their weights
+          constexpr uint32_t ID_S2 = KEYS ? umma_idesc_f16(QM, KT, 0, 0) : umma_idesc_bf16(QM, KT, 0, 0);
+#pragma unroll 1
+          for (int i = 0; NT > 0 && i <= NT; ++i) {
+            if (i < NT) {
+              if (!mbar_wait(KEYS ? kaready(ks_) : kfull(ks_), kp)) fail = 1;
+              if (KEYS && i > 0 && !(mbar_wait(staken(0), (i - 1) & 1) && mbar_wait(staken(1), (i - 1) & 1))) fail = 1;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t kd = umma_desc_add(dK, ks_ * C_::KV);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_bf16_ts(tmem + C_::t_s(i & 1), tmem + T_Q + kk * 8,
-                           umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S, kk > 0);
-            umma_commit(sfull(i & 1));
-            umma_commit(kfree(ks_));
+                for (int kk = 0; kk < D / 16; ++kk)
+                  umma_bf16_ts(tmem + C_::t_s(i & 1), tmem + T_Q + kk * 8,
+                               umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S2, kk > 0);
+                umma_commit(sfull(0, i & 1));
+                umma_commit(sfull(1, i & 1));
+                umma_commit(kfree(ks_));
+              }
+              __syncwarp();
+              if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
+            }
+            if (i > 0) {
+              const int j = i - 1, vs = j % NV;
+              if (!(mbar_wait(pfull(0, j & 1), (j >> 1) & 1) && mbar_wait(pfull(1, j & 1), (j >> 1) & 1))) fail = 1;
+              if (!mbar_wait(vfull(vs), (j / NV) & 1)) fail = 1;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t vd = umma_desc_add(dV, vs * C_::VST);
+#pragma unroll
+                for (int ks = 0; ks < KT / 16; ++ks)
+                  umma_bf16_ts(tmem + T_O, tmem + C_::t_p(j & 1, ks / 4) + (ks % 4) * 8,
+                               umma_desc_add(vd, ks * 16 * 128), ID_PV, ks > 0 || j > 0 ? 1u : 0u);
+                umma_commit(pvdone(0));
+                umma_commit(pvdone(1));
+                umma_commit(vfree(vs));
+              }
+              __syncwarp();
+            }
           }
-          __syncwarp();
-          if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
-          if (i > 0) mma_pv(i - 1);
+        } else {
+#pragma unroll 1
+          for (int i = 0; NT > 0 && i <= NT; ++i) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              if (i < NT) {
+                if (h == 0 && !mbar_wait(KEYS ? kaready(ks_) : kfull(ks_), kp)) fail = 1;
+                if (KEYS && i > 0 && !mbar_wait(staken(h), (i - 1) & 1)) fail = 1;
+                tc_fence_after();
+                if (elect_one()) {
+                  const uint64_t kd = umma_desc_add(dK, ks_ * C_::KV + h * (KT / 2) * 128);   // keys 64 h ..
+#pragma unroll
+                  for (int kk = 0; kk < D / 16; ++kk)
+                    umma_bf16_ts(tmem + C_::t_s(i & 1) + 64 * h, tmem + T_Q + kk * 8,
+                                 umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S, kk > 0);
+                  umma_commit(sfull(h, i & 1));
+                  if (h == 1) umma_commit(kfree(ks_));
+                }
+                __syncwarp();
+              }
+              if (i > 0) mma_pv(i - 1, h);
+            }
+            if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
+          }
         }
-        mma_pv(NT - 1);
-      } else if (w == W0 + 1 && lane == 0) {
+        if (NT > 0 && elect_one()) umma_commit(alldone);
+        __syncwarp();
+      } else if (w == W0 + 1) {
         // ========================================================== loads
+        if (lane == 0) {
+          s_fail = 0;
+          for (int s = 0; s < 3; ++s) {
+            mbar_init(kfull(s), KEYS ? 2 : 1);   // the loads, and with a key delta the tile's anchors
+            mbar_init(kfree(s), 1);
+            mbar_init(kaready(s), 8);
+          }
+          for (int s = 0; s < 2; ++s) {
+            mbar_init(vfull(s), 1);
+            mbar_init(vfree(s), 1);
+            mbar_init(lrfull(s), 1);
+            mbar_init(lrfree(s), 1);
+            for (int b = 0; b < 2; ++b) {
+              mbar_init(sfull(s, b), 1);
+              mbar_init(pfull(s, b), fold ? 2 : 4);
+            }
+            mbar_init(staken(s), fold ? 2 : 4);
+            mbar_init(dkfull(s), 1);
+            mbar_init(dkfree(s), 4);
+            mbar_init(pvdone(s), 1);
+          }
+          mbar_init(qready, NSM);
+          mbar_init(treeready, 1);
+          mbar_init(alldone, 1);
+          fence_mbar_init();
+          for (int i = 0; i < min(NK, NT); ++i) {
+            if (KEYS && i < NL) load_lrk(i);
+            load_k(i);
+            if (i < NV) load_v(i);
+          }
+        }
+        __syncwarp();
+        setup_sync();
+        // the tree, while the first tiles are on their way; a bad one's outputs are left unwritten
+        const bool ok = tree_masks_warp(
+            tp.parent ? tp.parent + ((int64_t)seq * tp.n_trees + tree) * n : nullptr, n, m, masks);
+        if (!ok) masks[lane] = masks[lane + 32] = 0;
+        if (lane == 0) s_bad = !ok;
+        __syncwarp();
+        if (lane == 0) {
+        mbar_arrive(treeready);
         // refills in the order the MMAs free the stages: dK and S of tile i, then P V of tile i - 1
         for (int i = 0; i < NT; ++i) {
           if (KEYS && i + NL < NT) {
@@ -340,49 +358,56 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             load_v(i - 1 + NV);
           }
         }
+        }
       } else if (KEYS && w == W0 + 2) {
         // ========================================================== dK
-        constexpr uint32_t ID_DK = umma_idesc_bf16(KT, 64, 0, 1);
+        constexpr uint32_t ID_DK = umma_idesc_bf16(KT, 2 * FP, 0, 1);
+        constexpr uint32_t BROW = 4 * FP, BPART = R * BROW;   // bytes of a B_k row's part, and of the part
+        setup_sync();
         const uint64_t dLRk = umma_desc(lrk_u, 16, 8 * C_::LR_ROWB, C_::LR_LAYOUT);
-        const uint64_t dBk = umma_desc(bk_u, R * 128, 1024, 2);
+        const uint64_t dBk = umma_desc(bk_u, BPART, 8 * BROW, BROW == 128 ? 2 : 4);
         for (int i = 0; i < NT; ++i) {
           if (!mbar_wait(lrfull(i % NL), (i / NL) & 1)) fail = 1;
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const int c = i * NH + h;
-            if (c > 0 && !mbar_wait(dkfree, (c - 1) & 1)) fail = 1;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            // the buffer's last part has been read: the other part's, or (two buffers) this one's
+            if (C_::NDK == 2 ? i > 0 : i + h > 0) {
+              const int o = C_::NDK == 2 ? h : 1 - h;
+              if (!mbar_wait(dkfree(o), (C_::NDK == 1 && h == 1 ? i : i - 1) & 1)) fail = 1;
+            }
             tc_fence_after();
             if (elect_one()) {
               const uint64_t lr = umma_desc_add(dLRk, (i % NL) * C_::LRK);
 #pragma unroll
               for (int ks = 0; ks < R / 16; ++ks)
-                umma_bf16(tmem + T_DK, umma_desc_add(lr, ks * 32),
-                          umma_desc_add(dBk, h * (R * 128) + ks * 16 * 128), ID_DK, ks > 0);
-              umma_commit(dkfull);
-              if (h == NH - 1) umma_commit(lrfree(i % NL));
+                umma_bf16(tmem + T_DK + (C_::NDK == 2 ? 2 * FP * h : 0), umma_desc_add(lr, ks * 32),
+                          umma_desc_add(dBk, h * BPART + ks * 16 * BROW), ID_DK, ks > 0);
+              umma_commit(dkfull(h));
+              if (h == 1) umma_commit(lrfree(i % NL));
             }
             __syncwarp();
           }
         }
       } else if (KEYS && w == W0 + 3) {
         // ========================================================== anchors s R(k0)
-        constexpr int NF = H2 / 32;   // frequencies a lane
-        double th[NF];
-#pragma unroll
-        for (int u = 0; u < NF; ++u) th[u] = rt.theta[lane + 32 * u];
+        // two adjacent frequencies a lane
+        const int f = 2 * lane < H2 ? 2 * lane : 0;
+        const double th0 = rt.theta[f], th1 = rt.theta[f + 1];
+        setup_sync();
         int ks_ = 0, kp = 1;
         for (int i = 0; i < NT; ++i) {
           if (i >= 3 && !mbar_wait(kaready(ks_), kp)) fail = 1;   // build(i - 3) has read its slot
           const int64_t k0 = n0 + i == Nc ? C : (int64_t)(n0 + i) * KT;
-#pragma unroll
-          for (int u = 0; u < NF; ++u) {
-            const float2 cs = rope_cs_exact(k0, th[u]);
-            anc[ks_ * 64 + lane + 32 * u] = make_float2(cs.x * p.s, cs.y * p.s);
-          }
+          const float2 a = rope_cs_exact(k0, th0), b = rope_cs_exact(k0, th1);
+          if (2 * lane < H2)
+            anc[ks_ * 32 + lane] = make_uint2(h2_bits(__floats2half2_rn(a.x * p.s, b.x * p.s)),
+                                              h2_bits(__floats2half2_rn(a.y * p.s, b.y * p.s)));
           __syncwarp();
           if (lane == 0) mbar_arrive(kfull(ks_));
           if (++ks_ == 3) { ks_ = 0; kp ^= 1; }
         }
+      } else {
+        setup_sync();
       }
       __syncwarp();
       cluster_sync_all();
@@ -391,102 +416,108 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       if constexpr (KEYS) regs_inc<112>();
       if (KEYS && w >= NSM) {
       // ============================================================ K^a build
-      const int gq = lane >> 2, t4 = lane & 3;
-      const int kb = 32 * sp + 16 * ((w - NSM) >> 2);   // this warp's 16 keys (its TMEM lanes)
-      // R(j) of keys kb + gq (+ 8) as (cos, cos) and (sin, sin) f16 pairs over two
-      // adjacent frequencies
-      uint32_t RC[2 * NH][2][2], RS[2 * NH][2][2];
+      // thread: key 32 sp + lane (its TMEM lane) and half h of the frequencies, in pairs
+      const int key = 32 * (w & 3) + lane, h = (w - NSM) >> 2;
+      uint32_t RC[FP / 2], RS[FP / 2];   // R(j): (cos, cos) and (sin, sin) of a pair, f16
+      // B_k^a's rows (past r, at r = 8, zeros) travel while R(j) is formed
+      constexpr int NBK = (R * D / 8 + 255) / 256;
+      const int bt = tid - 32 * NSM;
+      uint4 bkv[NBK];
+      const __nv_bfloat16* Bk = reinterpret_cast<const __nv_bfloat16*>(p.B_k) +
+                                (int64_t)agent0 * p.r * p.n_kv * D + kvh * D;
+#pragma unroll
+      for (int u = 0; u < NBK; ++u) {
+        const int i = bt + u * 256, j = i / (D / 8);
+        bkv[u] = make_uint4(0, 0, 0, 0);
+        if (j < p.r) bkv[u] = *reinterpret_cast<const uint4*>(Bk + (int64_t)j * p.n_kv * D + 8 * (i % (D / 8)));
+      }
+      if (bt < H2) thf[bt] = rt.thetaf[bt];
+      bar_sync(BAR_BUILD, 256);
       int ks_ = 0, kp = 0;
-      for (int i = 0; i < NT; ++i) {
+#pragma unroll 1
+      for (int i = 0; i < max(NT, 1); ++i) {
         const bool drafted = n0 + i == Nc;
-        if (i == 0 || drafted) {   // the drafted tile, a split's last: offsets are the nodes' depths
-          int j0 = kb + gq, j1 = j0 + 8;
-          if (drafted) {
-            j0 = j0 < m ? __popcll(masks[j0]) - 1 : 0;
-            j1 = j1 < m ? __popcll(masks[j1]) - 1 : 0;
-          }
-#pragma unroll
-          for (int q = 0; q < 2 * NH; ++q)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int f = 16 * q + 8 * u + 2 * t4;
-              const float th0 = thf[f], th1 = thf[f + 1];
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                const float j = (float)(hh ? j1 : j0);
-                const float2 a = sincos_small(j * th0), b = sincos_small(j * th1);
-                RC[q][hh][u] = h2_bits(__floats2half2_rn(a.x, b.x));
-                RS[q][hh][u] = h2_bits(__floats2half2_rn(a.y, b.y));
-              }
+        // R(j) at the first tile and at the drafted one (a split's last: offsets are the
+        // nodes' depths), before the set-up or, if it needs the tree, behind it
+#pragma unroll 1
+        for (int st = 0; (i == 0 || drafted) && st < 2; ++st) {
+          if (st == (int)drafted) {
+            int jo = key;
+            if (drafted) {
+              if (!mbar_wait(treeready, 0)) fail = 1;
+              jo = jo < m ? __popcll(masks[jo]) - 1 : 0;
             }
+            const float j = (float)jo;
+#pragma unroll
+            for (int k = 0; k < FP / 2; ++k) {
+              const float2 th = *reinterpret_cast<const float2*>(thf + FP * h + 2 * k);
+              const float2 a = sincos_small(j * th.x), b = sincos_small(j * th.y);
+              RC[k] = h2_bits(__floats2half2_rn(a.x, b.x));
+              RS[k] = h2_bits(__floats2half2_rn(a.y, b.y));
+            }
+          }
+          if (st == 0 && i == 0) {
+            // B_k^a as the dK MMA's operand: a part is R rows of FP + FP columns (its
+            // frequencies' two sides), swizzled over the row's bytes
+#pragma unroll
+            for (int u = 0; u < NBK; ++u) {
+              const int e = bt + u * 256, j = e / (D / 8), col = 8 * (e % (D / 8)), f = col % H2;
+              if (e < R * D / 8)
+                sts128(bk_u + (uint32_t)(f / FP) * (R * FP * 4) + tile_off<2 * FP, R>(j, (col / H2) * FP + f % FP),
+                       bkv[u].x, bkv[u].y, bkv[u].z, bkv[u].w);
+            }
+            fence_proxy_async_smem();
+            setup_sync();
+          }
         }
+        if (NT == 0) break;
         if (!mbar_wait(kfull(ks_), kp)) fail = 1;
-        const float2* an = anc + ks_ * 64;
-        // this lane's pair of K elements in a 128-byte-swizzled row: key kb + gq
-        // (+8), 16-byte chunk (2 q + u) ^ gq, word t4
-        const uint32_t rowb = k_u + ks_ * C_::KV + (uint32_t)(kb + gq) * 128 + 4 * t4;
-        constexpr uint32_t HI = KT * 128;   // columns + d/2: the next box, or (d = 64) 4 chunks on
-        auto at = [&](int q, int u, int hh) { return rowb + hh * 1024 + (uint32_t)(((2 * q + u) ^ gq) << 4); };
-        auto hi = [&](uint32_t o) { return D == 128 ? o + HI : o ^ 64; };
+        // dK's part as f16 pairs, x1 and x2 the two sides of the rotation
+        uint32_t x1[FP / 2], x2[FP / 2];
+        if (!mbar_wait(dkfull(h), i & 1)) fail = 1;
+        tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          uint32_t w1[2][2], w2[2][2];   // a quarter's base words, read together
-          auto base = [&](int q) {
+        for (int q = 0; q < FP / 16; ++q) {
+          uint32_t a[16], b[16];
+          const uint32_t td = tmem + T_DK + (C_::NDK == 2 ? 2 * FP * h : 0) + 16 * q + ((uint32_t)(32 * (w & 3)) << 16);
+          tmem_ld32x32b_x16(a, td);
+          tmem_ld32x32b_x16(b, td + FP);
+          tmem_wait_ld_r16(a);
+          tmem_wait_ld_r16(b);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                w1[u][hh] = lds32(at(q, u, hh));
-                w2[u][hh] = lds32(hi(at(q, u, hh)));
-              }
-          };
-          if (!mbar_wait(dkfull, (i * NH + h) & 1)) fail = 1;
-          tc_fence_after();
-          uint32_t xa[2][8], xb[2][8];   // 32 frequencies' two halves
-          const uint32_t tl = tmem + T_DK + ((uint32_t)kb << 16);
-          tmem_ld16x256_x2(xa[0], tl);
-          tmem_ld16x256_x2(xb[0], tl + 32);
-          tmem_ld16x256_x2(xa[1], tl + 16);
-          tmem_ld16x256_x2(xb[1], tl + 48);
-          tmem_wait_ld_regs(xa[0], xb[0]);
-          tmem_wait_ld_regs(xa[1], xb[1]);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(dkfree);   // the next part's MMA runs during this part's turn
-#pragma unroll
-          for (int qq = 0; qq < 2; ++qq) {
-            const int q = 2 * h + qq;
-            const uint32_t(&xl)[8] = xa[qq];
-            const uint32_t(&xh)[8] = xb[qq];
-            base(q);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int f = 16 * q + 8 * u + 2 * t4;
-              const float4 a = *reinterpret_cast<const float4*>(an + f);   // two adjacent (cos, sin)
-              const __half2 ac = __floats2half2_rn(a.x, a.z), as = __floats2half2_rn(a.y, a.w);
-              const __half2 nas = __hneg2(as);
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                const __half2 x1 = __floats2half2_rn(__uint_as_float(xl[4 * u + 2 * hh]),
-                                                     __uint_as_float(xl[4 * u + 2 * hh + 1]));
-                const __half2 x2 = __floats2half2_rn(__uint_as_float(xh[4 * u + 2 * hh]),
-                                                     __uint_as_float(xh[4 * u + 2 * hh + 1]));
-                const __half2 c = bits_h2(RC[q][hh][u]), sn = bits_h2(RS[q][hh][u]);
-                const __half2 y1 = __hfma2(x1, c, __hneg2(__hmul2(x2, sn)));   // R(j) dK
-                const __half2 y2 = __hfma2(x2, c, __hmul2(x1, sn));
-                // K_base + s R(k0) y, the base added inside the rotation's FMAs
-                w1[u][hh] = h2_bits(__hfma2(ac, y1, __hfma2(nas, y2, bf16x2_h2(w1[u][hh]))));
-                w2[u][hh] = h2_bits(__hfma2(ac, y2, __hfma2(as, y1, bf16x2_h2(w2[u][hh]))));
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                sts32(at(q, u, hh), w1[u][hh]);
-                sts32(hi(at(q, u, hh)), w2[u][hh]);
-              }
+          for (int c = 0; c < 16; c += 2) {
+            x1[8 * q + c / 2] = h2_bits(__floats2half2_rn(__uint_as_float(a[c]), __uint_as_float(a[c + 1])));
+            x2[8 * q + c / 2] = h2_bits(__floats2half2_rn(__uint_as_float(b[c]), __uint_as_float(b[c + 1])));
           }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dkfree(h));   // the next part's MMA runs during this part's turn
+        // eight frequencies at a time: a 16-byte chunk of each side of the key's swizzled
+        // row.  Side 2 is the next box, or (d = 64) four chunks on.
+        const uint32_t rowb = k_u + ks_ * C_::KV + (uint32_t)key * 128;
+        const uint4* an = reinterpret_cast<const uint4*>(anc + ks_ * 32 + FP / 2 * h);
+#pragma unroll
+        for (int c = 0; c < FP / 8; ++c) {
+          const uint32_t o1 = rowb + (uint32_t)(((FP / 8 * h + c) ^ (key & 7)) << 4);
+          const uint32_t o2 = D == 128 ? o1 + KT * 128 : o1 ^ 64;
+          const uint4 v1 = lds128(o1), v2 = lds128(o2);
+          const uint4 a01 = an[2 * c], a23 = an[2 * c + 1];
+          uint32_t w1[4] = {v1.x, v1.y, v1.z, v1.w}, w2[4] = {v2.x, v2.y, v2.z, v2.w};
+          const uint32_t ac4[4] = {a01.x, a01.z, a23.x, a23.z}, as4[4] = {a01.y, a01.w, a23.y, a23.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 u1 = bits_h2(x1[4 * c + e]), u2 = bits_h2(x2[4 * c + e]);
+            const __half2 cj = bits_h2(RC[4 * c + e]), sj = bits_h2(RS[4 * c + e]);
+            const __half2 ac = bits_h2(ac4[e]), as = bits_h2(as4[e]);
+            const __half2 y1 = __hfma2(u1, cj, __hneg2(__hmul2(u2, sj)));   // R(j) dK
+            const __half2 y2 = __hfma2(u2, cj, __hmul2(u1, sj));
+            // K_base + s R(k0) y, the base added inside the rotation's FMAs
+            w1[e] = h2_bits(__hfma2(ac, y1, __hfma2(__hneg2(as), y2, bf16x2_h2(w1[e]))));
+            w2[e] = h2_bits(__hfma2(ac, y2, __hfma2(as, y1, bf16x2_h2(w2[e]))));
+          }
+          sts128(o1, w1[0], w1[1], w1[2], w1[3]);
+          sts128(o2, w2[0], w2[1], w2[2], w2[3]);
         }
         fence_proxy_async_smem();   // the S MMA reads K^a through the async proxy
         __syncwarp();
@@ -502,13 +533,39 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       }
       } else {
       // ============================================================ softmax
+      // This thread's query row, in TMEM lane 32 sp + lane, and its half h of a tile's
+      // keys: two warps share a row block, h = 0 ahead of h = 1 by about half a tile's
+      // time, so that one weighs scores (bound by the SFU) while the other reads and
+      // stores.  A row's reference maximum is handed from one to the other, half after
+      // half; sums stay with each until the end.
+      // Folded (at most 64 rows): lanes 64.. repeat the rows and take the half h = 1 of
+      // every tile for themselves, with a maximum, a sum and outputs of their own that
+      // the merge joins like those of another split; the warps ch = 1 only help around
+      // the loop.
+      const int sp = w & 3, ch = w >> 2;
+      const int tl = 32 * sp + lane;
+      const int row = fold ? tl & 63 : tl;
+      const int h = fold ? tl >> 6 : ch;
+      const bool has = (fold ? 32 * (sp & 1) : 32 * sp) < rows;   // these lanes have rows
       const uint32_t tlane = (uint32_t)(32 * sp) << 16;
-      const uint64_t vis = has && row < rows ? masks[qnode] : 0;   // the drafted nodes this row sees
+      int qnode = 0;
+      uint32_t qv[D / 4];   // half a row's columns, packed
       if (has) {
+        int ag;
+        const int64_t off = locate(row < rows ? row : 0, qnode, ag);
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + off + H2 * ch);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint4 v = row < rows ? src[c] : make_uint4(0, 0, 0, 0);
+          qv[4 * c] = v.x; qv[4 * c + 1] = v.y; qv[4 * c + 2] = v.z; qv[4 * c + 3] = v.w;
+        }
         if constexpr (KEYS) {   // fp16 beside the fp16 K^a (bf16 values convert exactly within its range)
 #pragma unroll
           for (int c = 0; c < D / 4; ++c) qv[c] = h2_bits(bf16x2_h2(qv[c]));
         }
+      }
+      setup_sync();
+      if (has) {
         if constexpr (D == 128) {
           tmem_st32x32b_x32(tmem + T_Q + (D / 4) * ch + tlane, qv);
         } else {
@@ -518,7 +575,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
           uint32_t z[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) z[c] = 0;
-          tmem_st32x32b_x32(tmem + T_P + 32 * (1 - kh) + tlane, z);
+          tmem_st32x32b_x32(tmem + C_::t_p(0, 1 - h) + tlane, z);
         }
         tmem_wait_st();
       }
@@ -527,16 +584,16 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       if (lane == 0) mbar_arrive(qready);
 
       const float sl2 = p.scale * kLog2e;
-      float m_ref = -INFINITY, lsum = 0.f;
-      for (int i = 0; i < NT; ++i) {
+      float m_ref = -INFINITY, lsum = 0.f;   // m_ref: what this thread's sum refers to
+      for (int i = 0; i < NT && !(fold && ch == 1); ++i) {
         const bool drafted = n0 + i == Nc;
         const int cnt = drafted ? m : (int)min((int64_t)KT, C - (int64_t)(n0 + i) * KT);
         const int buf = i & 1;
-        if (!mbar_wait(sfull(buf), (i >> 1) & 1)) fail = 1;
+        if (!mbar_wait(sfull(h, buf), (i >> 1) & 1)) fail = 1;
         tc_fence_after();
         uint32_t sv[2][32];
-        if (live) {
-          const uint32_t ts = tmem + C_::t_s(buf) + 64 * kh + tlane;
+        if (has) {
+          const uint32_t ts = tmem + C_::t_s(buf) + 64 * h + tlane;
           tmem_ld32x32b_x32(sv[0], ts);
           tmem_ld32x32b_x32(sv[1], ts + 32);
           tmem_wait_ld_r32(sv[0]);
@@ -545,87 +602,99 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         if constexpr (KEYS) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(staken);   // S may be overwritten by the next tile's MMA
+          if (lane == 0) mbar_arrive(staken(h));   // these scores may be overwritten by the next tile's MMA
         }
         if (cnt < KT) {
           // rows behind the last key may hold anything: their values become zero
-          // (a weight of zero would not cover infinities)
+          // (a weight of zero would not cover infinities).  Each half's warps clear its rows.
           if (!mbar_wait(vfull(i % NV), (i / NV) & 1)) fail = 1;
           const uint32_t vst = v_u + (i % NV) * C_::VST;
           constexpr int CR = D / 8 + 8;   // 16-byte chunks a key
-          for (int e = tid; e < (KT - cnt) * CR; e += 32 * NSM) {
-            const int t = cnt + e / CR, c = e % CR;
+          const int t0 = max(cnt, 64 * h), nt = 64 * h + 64 - t0;
+          for (int e = fold ? tl & 63 : tl; e < nt * CR; e += fold ? 64 : 128) {
+            const int t = t0 + e / CR, c = e % CR;
             sts128(vst + (uint32_t)(c / 8) * (KT * 128) + t * 128 + (c % 8) * 16, 0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
-        if (live) {
-          if (drafted) {
-            // 64 nodes at most: this warp's half of the keys holds all of them or none
-            const uint64_t vm = kh == 0 ? vis : 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t v32 = (uint32_t)(vm >> (32 * h));
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!((v32 >> c) & 1u)) sv[h][c] = __float_as_uint(-INFINITY);
+        if (has) {
+          if (cnt < KT) {
+            // visible keys of this half: the drafted nodes this row sees (at most 64: in
+            // half 0), or those in front of the context's end
+            uint64_t vm = 0;
+            if (drafted) {
+              if (!mbar_wait(treeready, 0)) fail = 1;
+              if (h == 0 && row < rows) vm = masks[qnode];
+            } else {
+              const int v = cnt - 64 * h;
+              vm = v >= 64 ? ~0ull : (v > 0 ? (1ull << v) - 1 : 0);
             }
-          } else if (cnt < KT) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t v32 = (uint32_t)(vm >> (32 * k));
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                if (64 * kh + 32 * h + c >= cnt) sv[h][c] = __float_as_uint(-INFINITY);
+                if (!((v32 >> c) & 1u)) sv[k][c] = __float_as_uint(-INFINITY);
+            }
           }
           float mr[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float mx = __uint_as_float(sv[h][0]);
+          for (int k = 0; k < 2; ++k) {
+            float mx = __uint_as_float(sv[k][0]);
 #pragma unroll
-            for (int c = 1; c < 31; c += 2) mx = max3f(mx, __uint_as_float(sv[h][c]), __uint_as_float(sv[h][c + 1]));
-            mr[h] = fmaxf(mx, __uint_as_float(sv[h][31]));
+            for (int c = 1; c < 31; c += 2) mx = max3f(mx, __uint_as_float(sv[k][c]), __uint_as_float(sv[k][c + 1]));
+            mr[k] = fmaxf(mx, __uint_as_float(sv[k][31]));
           }
-          float mt = fmaxf(mr[0], mr[1]) * sl2;   // the scale is positive
-          if (!fold) {
-            float* xb = xch + buf * 256;
-            xb[w * 32 + lane] = mt;
-            bar_sync(BAR_PAIR + sp, 64);
-            mt = fmaxf(mt, xb[(w ^ 4) * 32 + lane]);
+          const float mt = fmaxf(mr[0], mr[1]) * sl2;   // the scale is positive
+          float ref = m_ref;   // the row's reference before this half
+          if (!fold && i + h > 0) {
+            bar_sync((h ? BAR_AB : BAR_BA) + sp, 64);
+            ref = xref[row];
           }
-          // lazy rescale: move the reference maximum only when a row's grew by > 8
-          const bool need = mt > m_ref + 8.f || (m_ref == -INFINITY && mt != -INFINITY);
-          if (__any_sync(0xffffffffu, need)) {
-            const float m_new = fmaxf(m_ref, mt);
-            const float corr = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
-            if (i > 0) {
-              // O holds every tile before this one (S of this tile is done, so P V of tile i - 2 is)
-              if (!mbar_wait(pvdone, (i - 1) & 1)) fail = 1;
-              tc_fence_after();
-              // O and O_lr behind it, 16 columns at a time: this warp's half, or folded all
-#pragma unroll 1
-              for (int h = fold ? 0 : ch; h < (D + R) / 16; h += fold ? 1 : 2) {
-                const uint32_t ta = tmem + T_O + 16 * h + tlane;
-                uint32_t ov[16];
-                tmem_ld32x32b_x16(ov, ta);
-                tmem_wait_ld_r16(ov);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * corr);
-                tmem_st32x32b_x16(ta, ov);
-              }
-              tmem_wait_st();
+          // lazy rescale: move the reference only when a row's maximum grew by > 8
+          const bool need = mt > ref + 8.f || (ref == -INFINITY && mt != -INFINITY);
+          const float m_new = need ? mt : ref;
+          if (__any_sync(0xffffffffu, need) && i + h > 0 && (i > 0 || !fold)) {
+            const float corr = ref == -INFINITY ? 0.f : fast_exp2(ref - m_new);
+            // O holds every half before this one, and no other is issued before this one's
+            // weights (folded: neither half of this tile).  S of this half is done, so the P V
+            // issued before it are, and the parities below are of the current phase or the last.
+            if (fold) {
+              if (!mbar_wait(pvdone(0), (i - 1) & 1)) fail = 1;
+              if (!mbar_wait(pvdone(1), (i - 1) & 1)) fail = 1;
+            } else if (!mbar_wait(pvdone(1 - h), (h ? i : i - 1) & 1)) {
+              fail = 1;
             }
-            lsum *= corr;
-            m_ref = m_new;
+            tc_fence_after();
+            // O and O_lr behind it, 16 columns at a time
+#pragma unroll 1
+            for (int k = 0; k < (D + R) / 16; ++k) {
+              const uint32_t ta = tmem + T_O + 16 * k + tlane;
+              uint32_t ov[16];
+              tmem_ld32x32b_x16(ov, ta);
+              tmem_wait_ld_r16(ov);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * corr);
+              tmem_st32x32b_x16(ta, ov);
+            }
+            tmem_wait_st();
+            tc_fence_before();
           }
+          if (!fold) {
+            xref[row] = m_new;
+            bar_arrive((h ? BAR_BA : BAR_AB) + sp, 64);
+          }
+          if (__any_sync(0xffffffffu, m_new != m_ref)) lsum *= m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
+          m_ref = m_new;
           const float mu = m_ref == -INFINITY ? 0.f : m_ref;
           const uint64_t scl = f2(sl2, sl2), nmu = f2(-mu, -mu);
           uint64_t acc = f2(0.f, 0.f);
           uint32_t pk[32];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
-              const uint64_t xa2 = fma_f2(f2(__uint_as_float(sv[h][c]), __uint_as_float(sv[h][c + 1])), scl, nmu);
+              const uint64_t xa2 = fma_f2(f2(__uint_as_float(sv[k][c]), __uint_as_float(sv[k][c + 1])), scl, nmu);
               float p0, p1;
               if (!KEYS && (c / 2) % kPolyEvery == 0) {
                 const float2 pp = f2_unpack(exp2_poly_f2(xa2));
@@ -637,69 +706,72 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
                 p1 = fast_exp2(xa.y);
               }
               acc = add_f2(acc, f2(p0, p1));
-              pk[16 * h + c / 2] = pack_bf16(p0, p1);
+              pk[16 * k + c / 2] = pack_bf16(p0, p1);
             }
           const float2 accf = f2_unpack(acc);
           lsum += accf.x + accf.y;
-          if (KEYS && i > 0) {   // P V of the last tile has read P
-            if (!mbar_wait(pvdone, (i - 1) & 1)) fail = 1;
+          if (KEYS && i > 0) {   // P V of this half's last weights has read them
+            if (!mbar_wait(pvdone(h), (i - 1) & 1)) fail = 1;
             tc_fence_after();
           }
-          tmem_st32x32b_x32(tmem + C_::t_p(buf) + 32 * kh + tlane, pk);
+          tmem_st32x32b_x32(tmem + C_::t_p(buf, h) + tlane, pk);
           if (!KEYS && fold) {   // P lies over the scores: no weights for the other half's keys
+            if (!mbar_wait(sfull(1 - h, buf), (i >> 1) & 1)) fail = 1;
+            tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 32; ++c) pk[c] = 0;
-            tmem_st32x32b_x32(tmem + C_::t_p(buf) + 32 * (1 - kh) + tlane, pk);
+            tmem_st32x32b_x32(tmem + C_::t_p(buf, 1 - h) + tlane, pk);
           }
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull(buf));
+        if (lane == 0) mbar_arrive(pfull(h, buf));
       }
 
       // ---- this split's partial: O as 16-byte chunks, chunk c of a row at c ^ (row mod
       // D / 4) (no bank conflicts by rows or by columns), O_lr, then m and l
       constexpr int NCH = D / 4;
       const uint32_t pol = k_u + C_::P_OL, pml = k_u + C_::P_ML;
+      if (NT > 0 && !mbar_wait(alldone, 0)) fail = 1;
+      if (has && NT > 0 && !fold) {
+        if (ch == 0) {   // the other half's last word on the reference
+          bar_sync(BAR_BA + sp, 64);
+          const float ref = xref[row];
+          lsum *= m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - ref);
+          m_ref = ref;
+        } else {
+          xsum[row] = lsum;
+        }
+        bar_sync(BAR_AB + sp, 64);
+        if (ch == 0) lsum += xsum[row];
+      }
+      if (has && ch == 0) {
+        sts32(pml + tl * 8, __float_as_uint(m_ref));
+        sts32(pml + tl * 8 + 4, __float_as_uint(lsum));
+      }
       if (NT > 0) {
-        // a warp that did not wait for every P V: S of the last tile is done, so P V is at
-        // tile NT - 2 or past it, and the parity of NT - 1 alone would be ambiguous
-        if (NT > 1 && !mbar_wait(pvdone, (NT - 2) & 1)) fail = 1;
-        if (!mbar_wait(pvdone, (NT - 1) & 1)) fail = 1;
         tc_fence_after();
         if (has) {
 #pragma unroll 1
-          for (int h = 0; h < H2 / 16; ++h) {
+          for (int k = 0; k < H2 / 16; ++k) {
             uint32_t ov[16];
-            tmem_ld32x32b_x16(ov, tmem + T_O + H2 * ch + 16 * h + tlane);
+            tmem_ld32x32b_x16(ov, tmem + T_O + H2 * ch + 16 * k + tlane);
             tmem_wait_ld_r16(ov);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              sts128(k_u + (uint32_t)tl * (D * 4) + (uint32_t)(((H2 * ch + 16 * h) / 4 + c) ^ (tl & (NCH - 1))) * 16,
+              sts128(k_u + (uint32_t)tl * (D * 4) + (uint32_t)(((H2 * ch + 16 * k) / 4 + c) ^ (tl & (NCH - 1))) * 16,
                      ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
           }
 #pragma unroll 1
-          for (int h = ch; h < R / 16; h += 2) {
+          for (int k = ch; k < R / 16; k += 2) {
             uint32_t ov[16];
-            tmem_ld32x32b_x16(ov, tmem + T_OL + 16 * h + tlane);
+            tmem_ld32x32b_x16(ov, tmem + T_OL + 16 * k + tlane);
             tmem_wait_ld_r16(ov);
 #pragma unroll
             for (int c = 0; c < 16; c += 4)
-              sts128(pol + (uint32_t)(tl * R + 16 * h + c) * 4, ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
+              sts128(pol + (uint32_t)(tl * R + 16 * k + c) * 4, ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
           }
-        }
-      }
-      if (live) {
-        if (!fold) {
-          float* lx = xch + (NT & 1) * 256;   // the exchange buffer the last tile did not use
-          lx[w * 32 + lane] = lsum;
-          bar_sync(BAR_PAIR + sp, 64);
-          lsum += lx[(w ^ 4) * 32 + lane];
-        }
-        if (ch == 0) {
-          sts32(pml + tl * 8, __float_as_uint(m_ref));
-          sts32(pml + tl * 8 + 4, __float_as_uint(lsum));
         }
       }
       }
@@ -715,7 +787,8 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       // partial i of a row: CTA i / F, lane row + 64 (i mod F) (F = 2 folded; 64 is a
       // multiple of the chunk swizzle's period)
       const int F = fold ? 2 : 1, np = S * F;
-      for (int r_ = split * share + w; r_ < r1; r_ += NW) {
+      if (!mbar_wait(treeready, 0)) fail = 1;
+      for (int r_ = split * share + w; r_ < r1 && !s_bad; r_ += NW) {
         const uint32_t ml = dsmem_addr(pml + 8 * (r_ + 64 * (lane & (F - 1))), lane < np ? lane / F : 0);
         const float mk = dsmem_ld(ml), lk = dsmem_ld(ml + 4);
         const uint32_t oa = k_u + (uint32_t)r_ * (D * 4) + (uint32_t)(c4 ^ (r_ & (NCH - 1))) * 16;
@@ -789,16 +862,6 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       }
       cluster_sync_all();   // the partials are read before any CTA of the cluster exits
     }
-  } else {
-    if (tid == 0) atomicOr(p.err, kDevTree);
-    if (w == W0 + 1 && lane == 0)   // the first loads land before the CTA ends
-      for (int i = 0; i < min(NK, NT); ++i) {
-        if (KEYS && i < NL && !mbar_wait(lrfull(i), 0)) fail = 1;
-        if (KEYS) mbar_arrive(kfull(i));   // in the anchors' place
-        if (!mbar_wait(kfull(i), 0)) fail = 1;
-        if (i < NV && !mbar_wait(vfull(i), 0)) fail = 1;
-      }
-  }
   if (fail) s_fail = 1;
   tc_fence_before();
   __syncthreads();
@@ -806,7 +869,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     tc_fence_after();
     tmem_dealloc(tmem, T_COLS);
   }
-  if (tid == 0 && s_fail) atomicOr(p.err, kDevPipeWait);
+  if (tid == 0 && (s_fail || s_bad)) atomicOr(p.err, (s_fail ? kDevPipeWait : 0) | (s_bad ? kDevTree : 0));
 }
 
 // ------------------------------------------------------------------ host
