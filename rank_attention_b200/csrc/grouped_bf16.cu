@@ -9,6 +9,8 @@
 //      two bf16 terms, t = hi + lo (the remainder: 2^-18 of t), which go back to
 //      TMEM as one operand of K = 2 r;
 //   3. out = y + s t B_a   M = 128, N = 64, over this CTA's share of the columns.
+// Where tiles are so few that clusters would leave SMs idle, several clusters form
+// the same t (grid z) and share the columns.
 // Both passes stream through one ring of stages (x and A_a, then y and B_a), so
 // that y and B_a are on their way while t is reduced.  Loads come in boxes of 32
 // rows, only those with rows of the tile; the other rows of a stage hold anything
@@ -67,6 +69,7 @@ __global__ void __launch_bounds__(GNTH)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int CS = gridDim.x, rank = blockIdx.x;
+  const int part = rank + CS * blockIdx.z, parts = CS * gridDim.z;   // this CTA's share of the columns
   const uint32_t red = sb + ns * C::STAGE;                 // [GM][R] fp32, CS > 1 only
   const int off_bar = ns * C::STAGE + (CS > 1 ? C::RED : 0);
   const uint32_t b0 = sb + off_bar;
@@ -99,24 +102,27 @@ __global__ void __launch_bounds__(GNTH)
     }
     fence_mbar_init();
   }
+  if (w == 3) tmem_alloc(smem_u32(tslot), G_COLS);
   if (w == 5 && lane == 0) {
     tma_prefetch(&tmX);
     tma_prefetch(&tmA);
     tma_prefetch(&tmY);
     tma_prefetch(&tmB);
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
   const SegTile t = s_tile;
-  if (t.bad) {   // the same verdict in every CTA
-    if (tid == 0) atomicOr(p.err, kDevSegment);
-    return;
-  }
-  if (t.rows == 0) return;   // the whole cluster: the same tile
   const int nblk = (p.n_out + GC - 1) / GC;   // column blocks, and this CTA's share
-  const int c0 = (int)((int64_t)nblk * rank / CS), c1 = (int)((int64_t)nblk * (rank + 1) / CS);
+  const int c0 = (int)((int64_t)nblk * part / parts), c1 = (int)((int64_t)nblk * (part + 1) / parts);
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + (int64_t)t.row0 * p.ldo;
-  if (t.agent < 0) {   // no adapter: out = y
-    if (p.out != p.y) {
+  // the same verdict in every CTA of the cluster: a bad segment, no such tile, or no
+  // adapter (out = y)
+  if (t.bad || t.rows == 0 || t.agent < 0) {
+    if (t.bad) {
+      if (tid == 0) atomicOr(p.err, kDevSegment);
+    } else if (t.rows > 0 && p.out != p.y) {
       const __nv_bfloat16* y = reinterpret_cast<const __nv_bfloat16*>(p.y) + (int64_t)t.row0 * p.ldy;
       const int lo = c0 * (GC / 8), n8 = min(c1 * (GC / 8), p.n_out / 8) - lo;   // 16-byte chunks
       for (int i = tid; i < t.rows * n8; i += GNTH) {
@@ -124,13 +130,9 @@ __global__ void __launch_bounds__(GNTH)
         *reinterpret_cast<uint4*>(out + row * p.ldo + c) = *reinterpret_cast<const uint4*>(y + row * p.ldy + c);
       }
     }
+    if (w == 3) tmem_dealloc(tmem, G_COLS);
     return;
   }
-  if (w == 4) tmem_alloc(smem_u32(tslot), G_COLS);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
   int fail = 0;
 
   const int chunks = (p.hidden + GC - 1) / GC;
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(GNTH)
   if (fail) s_fail = 1;
   tc_fence_before();
   __syncthreads();
-  if (w == 4) {
+  if (w == 3) {
     tc_fence_after();
     tmem_dealloc(tmem, G_COLS);
   }
@@ -384,6 +386,10 @@ cudaError_t launch_gt(const GroupedParams& p, cudaStream_t st) {
   // CTAs a tile: as many as keep the launch within about two CTAs an SM
   int CS = 8;
   while (CS > 1 && tiles * CS > 2 * 148) CS /= 2;
+  // clusters a tile: those that would otherwise leave SMs idle form t again and share
+  // the columns, down to two blocks of 64 a CTA
+  int Z = 1;
+  while (Z < 8 && tiles * CS * Z * 2 <= 148 && (int64_t)CS * Z * 4 * GC <= p.n_out) Z *= 2;
   // as many stages as let two CTAs share an SM
   const int rest = 1024 + (CS > 1 ? C::RED : 0) + C::MISC;
   int ns = (113 * 1024 - rest) / C::STAGE;
@@ -401,7 +407,7 @@ cudaError_t launch_gt(const GroupedParams& p, cudaStream_t st) {
     allowed[dev & 63] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)CS, (unsigned)tiles, 1);
+  cfg.gridDim = dim3((unsigned)CS, (unsigned)tiles, (unsigned)Z);
   cfg.blockDim = dim3(GNTH);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;

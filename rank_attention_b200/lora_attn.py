@@ -439,7 +439,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _on_device(device: int, stream, where: str) -> int:
     """The stream to launch on; the arguments' device must be the current one."""
-    if torch.cuda.current_device() != device:
+    if torch._C._cuda_getDevice() != device:
         raise ValueError(f"{where}: tensors are on cuda:{device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if stream is None:   # without building a Stream object (about 2 us a call)
