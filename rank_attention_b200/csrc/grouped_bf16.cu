@@ -383,9 +383,13 @@ cudaError_t launch_gt(const GroupedParams& p, cudaStream_t st) {
   if (!grouped_maps(p, R, &mx, &ma, &my, &mb)) return cudaErrorInvalidValue;
   // every segment ends in at most one short tile
   const int64_t tiles = (int64_t)(p.n_tokens + GM - 1) / GM + p.n_segs;
-  // CTAs a tile: as many as keep the launch within about two CTAs an SM
+  // CTAs a tile: eight or four while one CTA an SM covers the launch, two while two do.
+  // The sum over distributed shared memory grows with CS: 16384 tokens, r 64, 132 tiles
+  // at CS 1 / 2 / 4 / 8: 90 / 77 / 99 / 203 us; 1501 tokens, r 32, 21 tiles: 42 / 25 /
+  // 17.8 / 18.9 us; 48 tokens, r 16, 4 tiles (one cluster a tile): 64 / 35 / 20 / 13 us.
   int CS = 8;
-  while (CS > 1 && tiles * CS > 2 * 148) CS /= 2;
+  while (CS > 2 && tiles * CS > 148) CS /= 2;
+  if (tiles * CS > 2 * 148) CS = 1;
   // clusters a tile: those that would otherwise leave SMs idle form t again and share
   // the columns, down to two blocks of 64 a CTA
   int Z = 1;
