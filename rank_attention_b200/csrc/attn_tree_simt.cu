@@ -109,12 +109,13 @@ __global__ void __launch_bounds__(NTH)
   const float* Bv = reinterpret_cast<const float*>(p.B_v) + (int64_t)agent * R * ldB + kvh * D;
   const int64_t qrow0 = ((int64_t)seq * p.n_agents + agent) * p.n_q_tokens + tok0;
 
-  for (int i = tid; i < RB * D; i += NTH) {
-    const int row = i / D, c = i % D;
-    float q = 0.f;
+  for (int i = tid; i < RB * D / 4; i += NTH) {
+    const int row = i / (D / 4), c = 4 * (i % (D / 4));
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < rows)
-      q = reinterpret_cast<const float*>(p.q)[((qrow0 + row / g) * p.n_q + kvh * g + row % g) * D + c];
-    Qs[row * LD + c] = q;
+      q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) +
+                                           ((qrow0 + row / g) * p.n_q + kvh * g + row % g) * D + c);
+    *reinterpret_cast<float4*>(Qs + row * LD + c) = q;
   }
   for (int i = tid; i < TK * H2; i += NTH) CS[i] = rope_cs_exact(i / H2, rt.theta[i % H2]);
   uint64_t vis[4];   // the drafted nodes this thread's rows see
@@ -144,19 +145,22 @@ __global__ void __launch_bounds__(NTH)
     const int cnt = (int)min((int64_t)TK, (drafted ? (int64_t)m : C) - k0);
     const int64_t row0 = drafted ? C + (int64_t)tree * tp.nodes + k0 : k0;
     __syncthreads();   // the last tile's reads are done
-    for (int i = tid; i < TK * D; i += NTH) {
-      const int t = i / D, c = i % D;
-      float kv = 0.f, vv = 0.f;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < TK * D / 4 / NTH; ++u) {
+      const int i = tid + u * NTH, t = i / (D / 4), c = 4 * (i % (D / 4));
+      float4 kv = zero, vv = zero;
       if (t < cnt) {
-        kv = kbase[(row0 + t) * p.kv_tok + c];
-        vv = vbase[(row0 + t) * p.kv_tok + c];
+        kv = *reinterpret_cast<const float4*>(kbase + (row0 + t) * p.kv_tok + c);
+        vv = *reinterpret_cast<const float4*>(vbase + (row0 + t) * p.kv_tok + c);
       }
-      Ka[t * LD + c] = kv;
-      Vs[t * LD + c] = vv;
+      *reinterpret_cast<float4*>(Ka + t * LD + c) = kv;
+      *reinterpret_cast<float4*>(Vs + t * LD + c) = vv;
     }
-    for (int i = tid; i < TK * 2 * R; i += NTH) {
-      const int t = i / (2 * R), c = i % (2 * R);
-      LRs[t * LDR + c] = t < cnt ? lrp[(row0 + t) * 2 * R + c] : 0.f;
+    for (int i = tid; i < TK * 2 * R / 4; i += NTH) {
+      const int t = i / (R / 2), c = 4 * (i % (R / 2));
+      *reinterpret_cast<float4*>(LRs + t * LDR + c) =
+          t < cnt ? *reinterpret_cast<const float4*>(lrp + (row0 + t) * 2 * R + c) : zero;
     }
     if (Bk) {
       if (tid < H2) Anc[tid] = rope_cs_exact(drafted ? C : k0, rt.theta[tid]);
@@ -343,13 +347,13 @@ cudaError_t launch_ts(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   const auto kern = attn_tree_simt_kernel<OUT, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
   if (e != cudaSuccess) return e;
-  // splits: enough CTAs for two an SM, at least two tiles a split, at most the
+  // splits: enough CTAs for two an SM, at least a tile a split, at most the
   // portable cluster size
   const int QB = RB / p.g, nblk = (p.n_q_tokens + QB - 1) / QB;
   const int64_t units = (int64_t)nblk * p.n_agents * p.n_kv * p.n_seqs;
   const int64_t tiles = (p.max_kv_len + TK - 1) / TK + 1;
   int S = 1;
-  while (S < 8 && units * S < 2 * 148 && tiles >= 4 * S) S *= 2;
+  while (S < 8 && units * S < 2 * 148 && tiles > S) S *= 2;
   p.n_splits = S;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, (unsigned)(nblk * p.n_agents * p.n_kv), (unsigned)p.n_seqs);
