@@ -111,9 +111,149 @@ __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p
   }
 }
 
+// The same over tiles of 64 rows, where segments are long enough to fill them: both
+// products as register tiles of 4 x 4 (16 FMAs for two 16-byte shared-memory reads).
+constexpr int WM = 64, WK = 32, WN = 64;
+
+// acc[4][4] += rows of a (4 ty ..) x columns of b (4 tx ..) over n steps
+template <int LA, int LB>
+__device__ __forceinline__ void tile_fma(float (&acc)[4][4], const float (*a)[LA], const float (*b)[LB], int ty, int tx,
+                                         int n) {
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) {
+    const float4 u = *reinterpret_cast<const float4*>(&a[k][4 * ty]);
+    const float4 v = *reinterpret_cast<const float4*>(&b[k][4 * tx]);
+    const float av[4] = {u.x, u.y, u.z, u.w}, bv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+  }
+}
+
+__global__ void __launch_bounds__(NTH) grouped_wide_kernel(const GroupedParams p) {
+  __shared__ __align__(16) float xs[WK][WM + 4];   // x, transposed
+  __shared__ __align__(16) float ws[64][WN + 4];   // A_a's rows (WK), then B_a's (r)
+  __shared__ __align__(16) float ts[64][WM + 4];   // x A_a, transposed: this CTA's share, then the sum
+  __shared__ SegTile s_tile;
+  const int tid = threadIdx.x, rank = blockIdx.x, R = p.r;
+  if (tid < 32) {
+    const SegTile t = find_seg_tile(p, blockIdx.y, WM);
+    if (tid == 0) s_tile = t;
+  }
+  __syncthreads();
+  const SegTile t = s_tile;
+  if (t.bad) {
+    if (tid == 0) atomicOr(p.err, kDevSegment);
+    return;
+  }
+  if (t.rows == 0) return;   // the whole cluster: the same tile
+  const float* y = reinterpret_cast<const float*>(p.y) + (int64_t)t.row0 * p.ldy;
+  float* out = reinterpret_cast<float*>(p.out) + (int64_t)t.row0 * p.ldo;
+  const int nb = (p.n_out + WN - 1) / WN, b0 = nb * rank / CS, b1 = nb * (rank + 1) / CS;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  // thread: rows 4 ty .. +3, ranks or columns 4 tx .. +3
+  const int ty = tid >> 4, tx = tid & 15;
+  const bool low = 4 * tx < R;   // this thread has ranks
+  float acc[4][4] = {};
+  if (t.agent >= 0) {
+    const float* x = reinterpret_cast<const float*>(p.x) + (int64_t)t.row0 * p.ldx;
+    const float* A = reinterpret_cast<const float*>(p.A) + t.agent * p.a_agent;
+    const int chunks = (p.hidden + WK - 1) / WK, ch0 = chunks * rank / CS, ch1 = chunks * (rank + 1) / CS;
+    // the next chunk's words travel while this one's are multiplied: x 64 rows x 8
+    // float4, A_a 32 rows x 16, two of each a thread
+    float4 xv[2], av[2];
+    auto fetch = [&](int ch) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = tid + u * NTH, row = i >> 3, k = ch * WK + 4 * (i & 7);
+        xv[u] = row < t.rows && k < p.hidden ? *reinterpret_cast<const float4*>(x + row * p.ldx + k) : zero;
+        const int kk = ch * WK + (i >> 4), c = 4 * (i & 15);
+        av[u] = kk < p.hidden && c < R ? *reinterpret_cast<const float4*>(A + (int64_t)kk * R + c) : zero;
+      }
+    };
+    if (ch0 < ch1) fetch(ch0);
+    for (int ch = ch0; ch < ch1; ++ch) {
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = tid + u * NTH, row = i >> 3, k = 4 * (i & 7);
+        xs[k][row] = xv[u].x;
+        xs[k + 1][row] = xv[u].y;
+        xs[k + 2][row] = xv[u].z;
+        xs[k + 3][row] = xv[u].w;
+        *reinterpret_cast<float4*>(&ws[i >> 4][4 * (i & 15)]) = av[u];
+      }
+      __syncthreads();
+      if (ch + 1 < ch1) fetch(ch + 1);
+      if (low) tile_fma(acc, xs, ws, ty, tx, WK);
+    }
+    if (low) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(&ts[4 * tx + j][4 * ty]) = make_float4(acc[0][j], acc[1][j], acc[2][j], acc[3][j]);
+    }
+    ptx::cluster_sync_all();   // (the agent is the whole cluster's)
+    float4 sum[4];
+    if (low) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[j] = zero;
+        const uint32_t a = ptx::smem_u32(&ts[4 * tx + j][4 * ty]);
+#pragma unroll
+        for (int k = 0; k < CS; ++k) {
+          const float4 v = ptx::dsmem_ld4(ptx::dsmem_addr(a, k));
+          sum[j].x += v.x; sum[j].y += v.y; sum[j].z += v.z; sum[j].w += v.w;
+        }
+      }
+    }
+    ptx::cluster_sync_all();   // every share is read before the sum lies over it, or its CTA exits
+    if (low) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(&ts[4 * tx + j][4 * ty]) = sum[j];
+    }
+  } else if (p.out == p.y) {
+    return;   // no adapter, in place
+  }
+  const float* B = reinterpret_cast<const float*>(p.B) + (int64_t)max(t.agent, 0) * R * p.n_out;
+  for (int b = b0; b < b1; ++b) {
+    const int col = b * WN + 4 * tx;
+    const bool in = col < p.n_out;   // n_out is a multiple of 4
+    float4 yv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      yv[i] = in && 4 * ty + i < t.rows ? *reinterpret_cast<const float4*>(y + (4 * ty + i) * p.ldy + col) : zero;
+    if (t.agent >= 0) {
+      __syncthreads();   // ts is in place, the last block's B_a has been read
+      for (int i = tid; i < R * (WN / 4); i += NTH) {
+        const int j = i >> 4, c = b * WN + 4 * (i & 15);
+        *reinterpret_cast<float4*>(&ws[j][4 * (i & 15)]) =
+            c < p.n_out ? *reinterpret_cast<const float4*>(B + (int64_t)j * p.n_out + c) : zero;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+      tile_fma(acc, ts, ws, ty, tx, R);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        yv[i] = make_float4(fmaf(p.s, acc[i][0], yv[i].x), fmaf(p.s, acc[i][1], yv[i].y),
+                            fmaf(p.s, acc[i][2], yv[i].z), fmaf(p.s, acc[i][3], yv[i].w));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (in && 4 * ty + i < t.rows) *reinterpret_cast<float4*>(out + (4 * ty + i) * p.ldo + col) = yv[i];
+  }
+}
+
 cudaError_t launch_grouped_simt(const GroupedParams& p, cudaStream_t st) {
+  // 64-row tiles where segments have 64 rows on average (their sizes are known only
+  // on the device), else 16-row ones
+  const bool wide = p.n_tokens >= (int64_t)WM * p.n_segs;
+  const int tm = wide ? WM : TM;
   // every segment ends in at most one short tile
-  const int64_t tiles = (int64_t)(p.n_tokens + TM - 1) / TM + p.n_segs;
+  const int64_t tiles = (int64_t)(p.n_tokens + tm - 1) / tm + p.n_segs;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CS, (unsigned)tiles, 1);
   cfg.blockDim = dim3(NTH);
@@ -125,7 +265,7 @@ cudaError_t launch_grouped_simt(const GroupedParams& p, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, grouped_simt_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, wide ? grouped_wide_kernel : grouped_simt_kernel, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
