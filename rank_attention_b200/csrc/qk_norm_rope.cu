@@ -9,10 +9,11 @@
 // accesses at i and i + d/2 in bf16), so a pair is turned inside one thread and
 // the sum of squares needs three shuffles.  (cos, sin) are formed once per token
 // and CTA (angle reduced in fp64), shared by all its heads, and laid down with the norm
-// weights folded in.  Two head rows in flight a thread and 64 registers (four CTAs
-// an SM) measured best: 4096 tokens x (4 agents x 32 + 8) heads, 302 MB, 64.7 us
-// (4.67 TB/s, 71 % of the copy rate); four rows at 80 registers 66.0 us, two sets
-// of rows turn about 75-82 us (they spill).
+// weights folded in.  Two head rows in flight a thread, 64 registers and eight CTAs
+// of 128 threads an SM measured best: 4096 tokens x (4 agents x 32 + 8) heads, 302 MB,
+// 57.8 us (5.2 TB/s, 80 % of the copy rate); four CTAs of 256 threads 63.0 us, four
+// rows at 80 registers 66.0 us, two sets of rows taking turns 75-82 us (they spill).
+// A verification step's 16 tokens take 3.5 us, which is latency.
 #include <cmath>
 
 #include "bf16_common.cuh"
@@ -22,8 +23,8 @@
 namespace la {
 namespace {
 
-constexpr int NTH = 256;
-constexpr int kMaxTB = 4;   // tokens per CTA
+constexpr int NTH = 128;
+constexpr int kMaxTB = 2;   // tokens per CTA
 constexpr int kUnr = 2;     // head rows a thread has in flight
 
 struct QkParams {
@@ -94,7 +95,7 @@ struct Raw8<float> {
 };
 
 template <typename IO, int D>
-__global__ void __launch_bounds__(NTH, 4)
+__global__ void __launch_bounds__(NTH, 8)
     qk_norm_rope_kernel(const QkParams p, const TreeParams tp, const __grid_constant__ RopeTheta rt) {
   constexpr int LPH = D / 16, RPP = NTH / LPH;   // lanes per head row, head rows a pass
   // per token the turned pair's four factors: w1 cos, w2 sin, w2 cos, w1 sin
@@ -113,10 +114,12 @@ __global__ void __launch_bounds__(NTH, 4)
                       : reinterpret_cast<const IO*>(p.k) + seq * p.kv_in_seq + unit * p.kv_in_tree;
   const int64_t src_tok = isq ? p.q_tok : p.kv_in_tok;
   const int slots = min(p.tb, p.n_tok - tok0) * H;   // head rows of the CTA's tokens, live or not
-  // idx / H for idx < kMaxTB H: (idx + 1/2) / H lies 1 / (2 H) off the whole numbers,
-  // far above the product's rounding
-  const float inv_h = 1.f / (float)H;
-  auto token = [&](int idx) { return (int)(((float)idx + 0.5f) * inv_h); };
+  auto token = [&](int idx) {   // idx / H for idx < kMaxTB H
+    int t = 0;
+#pragma unroll
+    for (int k = 1; k < kMaxTB; ++k) t += idx >= k * H;
+    return t;
+  };
   Raw8<IO> lo[kUnr], hi[kUnr];
   auto fetch = [&](int base) {
 #pragma unroll
@@ -233,8 +236,8 @@ cudaError_t launch_qk(const QkParams& pin, const TreeParams& tp, double rope_bas
   RopeTheta rt = {};
   rope_thetas(rope_base, D, &rt);
   const int slots = p.q_slots + (p.k ? tp.n_trees : 0);
-  // four tokens a CTA (one angle a thread in bf16 at d = 128), one where that
-  // would leave SMs without a CTA
+  // two tokens a CTA (one angle a thread at d = 128), one where that would leave
+  // SMs without a CTA
   p.tb = (int64_t)((p.n_tok + kMaxTB - 1) / kMaxTB) * slots * p.n_seqs >= 148 ? kMaxTB : 1;
   const dim3 grid((unsigned)((p.n_tok + p.tb - 1) / p.tb), (unsigned)slots, (unsigned)p.n_seqs);
   qk_norm_rope_kernel<IO, D><<<grid, NTH, 0, st>>>(p, tp, rt);
