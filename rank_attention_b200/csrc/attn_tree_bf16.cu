@@ -607,6 +607,13 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         if (cnt < KT) {
           // rows behind the last key may hold anything: their values become zero
           // (a weight of zero would not cover infinities).  Each half's warps clear its rows.
+          if (NV == 1 && i > 0) {
+            // the one stage holds the last tile until its P V is done (two stages: the tile
+            // before it, whose P V came before these scores).  Of half 0's at h = 1 that is
+            // known, and its barrier may be a phase further.
+            if (!mbar_wait(pvdone(1), (i - 1) & 1)) fail = 1;
+            if ((fold || h == 0) && !mbar_wait(pvdone(0), (i - 1) & 1)) fail = 1;
+          }
           if (!mbar_wait(vfull(i % NV), (i / NV) & 1)) fail = 1;
           const uint32_t vst = v_u + (i % NV) * C_::VST;
           constexpr int CR = D / 8 + 8;   // 16-byte chunks a key

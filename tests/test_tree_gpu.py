@@ -183,6 +183,14 @@ def test_bf16_long_context_many_splits(la):
     run(la, A=1, kv=1, ctx=(6001,), n=40, keys=False, seed=7)
 
 
+@pytest.mark.parametrize("n", [13, 27])   # folded, and with two warps a row
+def test_bf16_one_value_stage_many_tiles(la, n):
+    """r = 64 leaves one V stage: a long unsplit run of tiles ends in a partial
+    context tile and the drafted one, whose dead rows are cleared in that stage."""
+    for seed in range(2):
+        run(la, S=3, A=4, kv=8, r=64, ctx=(2999, 1777, 2421), n=n, per_agent=True, lens=(13, 9, 2, 7, 12), seed=seed)
+
+
 def test_bf16_fp32_out(la):
     run(la, out_dtype=torch.float32, ctx=(300,), n=5, seed=8)
 
