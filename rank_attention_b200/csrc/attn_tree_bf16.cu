@@ -524,7 +524,9 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         if (lane == 0) mbar_arrive(kaready(ks_));
         if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
       }
-      // B_v^a for the merge over B_k^a, which the last dK has read
+      // B_v^a for the merge over B_k^a, once the last tile's dK has read it (both parts:
+      // part 1 is issued last, and is at the last tile or behind it by now)
+      if (NT > 0 && !mbar_wait(dkfull(1), (NT - 1) & 1)) fail = 1;
       const __nv_bfloat16* Bv = reinterpret_cast<const __nv_bfloat16*>(p.B_v) +
                                 (int64_t)agent0 * p.r * p.n_kv * D + kvh * D;
       for (int i = tid - 32 * NSM; i < p.r * D / 8; i += 256) {

@@ -183,6 +183,23 @@ def test_bf16_long_context_many_splits(la):
     run(la, A=1, kv=1, ctx=(6001,), n=40, keys=False, seed=7)
 
 
+@pytest.mark.parametrize("r", [16, 32, 64])
+@pytest.mark.parametrize("n", [8, 32])
+def test_bf16_repeats_are_identical(la, r, n):
+    """The merge's up-projection takes the place of the key's one only once every
+    read of that is over: thirty launches in a row give the same bits."""
+    i = make(S=4, A=3, kv=2, g=3, r=r, ctx=(1450, 700, 1101, 481), n=n, per_agent=True, garbage=False, seed=r + n)
+    args, tree, out, keep = launch(la, i)
+    la.lora_attn_tree(args, tree)
+    torch.cuda.synchronize()
+    check(la, i, out, torch.bfloat16)
+    first = out.clone()
+    for _ in range(30):
+        out.fill_(SENT)
+        la.lora_attn_tree(args, tree)
+        assert torch.equal(out, first)
+
+
 @pytest.mark.parametrize("n", [13, 27])   # folded, and with two warps a row
 def test_bf16_one_value_stage_many_tiles(la, n):
     """r = 64 leaves one V stage: a long unsplit run of tiles ends in a partial
