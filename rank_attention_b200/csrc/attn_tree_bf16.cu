@@ -971,15 +971,20 @@ cudaError_t launch_tt(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
       res[k] = c > 0 ? c : (k == 1 ? 1 : -1);
     }
   }
-  // splits: the least waves x (tiles of a split + the tiles' worth of a CTA's
-  // start and merge)
+  // splits: the least waves x (tiles of a split + the tiles' worth of a CTA's start and
+  // hand-over + that of merging its rows, a warp a row at a time).  Measured in tiles: a
+  // row of a warp 1.4 without a key delta (1.5 us; 96 rows over 100 keys: 2 splits 17.9
+  // us, 5 12.8 us, 8 11.7 us), about 1 with.  A split without keys still merges its share.
   const int64_t units = (int64_t)ny * p.n_seqs, tiles = (p.max_kv_len + KT - 1) / KT + 1;
-  constexpr double kFixed = 5.0;
+  const int rows = (int)min((int64_t)QM, (int64_t)tp.nodes * p.g * (pooled ? p.n_agents : 1));
+  constexpr double kFixed = 5.0, kRow = KEYS ? 1.0 : 1.4;
+  constexpr int kMergeWarps = NSM + C::NB;
   int S = 1;
   double best = 0;
   for (int k = 1; k <= kMaxSplits; ++k) {
-    if (res[k] < 1 || (k > 1 && k > tiles)) continue;
-    const double t = (double)((units + res[k] - 1) / res[k]) * ((tiles + k - 1) / k + kFixed);
+    if (res[k] < 1) continue;
+    const int share = ((rows + k - 1) / k + kMergeWarps - 1) / kMergeWarps;
+    const double t = (double)((units + res[k] - 1) / res[k]) * ((tiles + k - 1) / k + kFixed + kRow * share);
     if (k == 1 || t < best - 1e-9) {
       best = t;
       S = k;
