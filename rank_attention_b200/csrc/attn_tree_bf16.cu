@@ -16,11 +16,23 @@
 // Without a key delta (KEYS = false) K_base is the operand as it lies, in bf16,
 // and the scores are double-buffered, P lying over the scores it came from.
 //
-// Warps: eight softmax warps (two per TMEM sub-partition, 64 keys each), eight
-// build warps (a thread: one key, half the frequencies), and one warp each to issue S and P V, to load, to
-// issue dK (a part's MMA runs while the build turns the part before), and to form the anchors
-// s R(k0) in fp64.  The running maximum is rescaled lazily (O and l corrected
-// only when a row's maximum grows by more than 2^8).
+// Warps: eight softmax warps (two per TMEM sub-partition), eight build warps (a
+// thread: one key, half the frequencies), and one warp each to issue S and P V, to
+// load, to issue dK (a part's MMA runs while the build turns the part before), and
+// to form the anchors s R(k0) in fp64.  The reference maximum is moved lazily (O and
+// l corrected only when a row's maximum grows by more than 2^8).
+//
+// What bounds it (one B200).  16 nodes of 3 agents over 8192 keys (r 16, 32 / 8 heads,
+// 24 x 5 CTAs): 34.6 us, of it 1.5 us a tile, 13 tiles a CTA, and about 15 us around
+// them (launch, cold instructions, the first tile's way through the pipeline, the
+// cluster's merge).  With the softmax's arithmetic left out a tile takes 1.3 us, with
+// the build's too 0.97 us: three chains of dependent steps (load, dK, build, S;
+// softmax; P V) share the SM's shared-memory bandwidth (212 KB a tile) and issue
+// slots; the tensor pipe is active 23 %.  Without a key delta a tile takes 1.1 us.
+// Measured and not kept: P over the scores with a key delta (dK's parts
+// double-buffered in the columns won: folded tiles 2.0 us), dK in a ring of four
+// parts (1.5 us), folded halves split over two warps (1.5 us), tiles prefetched into
+// L2 ahead of the stages (no change), one lane polling for its warp (1.4x slower).
 #include <cmath>
 
 #include "attn_tc_common.cuh"
@@ -204,144 +216,144 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
   int fail = 0;
 
   if (w >= W0) {
-      if constexpr (KEYS) regs_dec<32>();
-      if (w == W0) {
-        // ========================================================== S and P V
-        // (the whole warp walks the loop and one elected lane issues: descriptors
-        // stay in uniform registers, about 75 cycles an MMA instead of 95)
-        constexpr uint32_t ID_S = KEYS ? umma_idesc_f16(QM, KT / 2, 0, 0) : umma_idesc_bf16(QM, KT / 2, 0, 0);
-        constexpr uint32_t ID_PV = umma_idesc_bf16(QM, D + R, 0, 1);
-        tmem_alloc(smem_u32(tslot), T_COLS);
-        setup_sync();
-        const uint64_t dK = umma_desc(k_u, 16, 1024, 2);
-        const uint64_t dV = umma_desc(v_u, KT * 128, 1024, 2);
-        auto mma_pv = [&](int i, int h) {   // O, O_lr += P [V_base | LRv] over half h of tile i
-          const int vs = i % NV;
-          if (!mbar_wait(pfull(h, i & 1), (i >> 1) & 1)) fail = 1;
-          if (h == 0 && !mbar_wait(vfull(vs), (i / NV) & 1)) fail = 1;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t vd = umma_desc_add(dV, vs * C_::VST + h * (KT / 2) * 128);
-            const uint32_t tP = tmem + C_::t_p(i & 1, h), acc = i > 0 || h > 0 ? 1u : 0u;
+    if constexpr (KEYS) regs_dec<32>();
+    if (w == W0) {
+      // ========================================================== S and P V
+      // (the whole warp walks the loop and one elected lane issues: descriptors
+      // stay in uniform registers, about 75 cycles an MMA instead of 95)
+      constexpr uint32_t ID_S = KEYS ? umma_idesc_f16(QM, KT / 2, 0, 0) : umma_idesc_bf16(QM, KT / 2, 0, 0);
+      constexpr uint32_t ID_PV = umma_idesc_bf16(QM, D + R, 0, 1);
+      tmem_alloc(smem_u32(tslot), T_COLS);
+      setup_sync();
+      const uint64_t dK = umma_desc(k_u, 16, 1024, 2);
+      const uint64_t dV = umma_desc(v_u, KT * 128, 1024, 2);
+      auto mma_pv = [&](int i, int h) {   // O, O_lr += P [V_base | LRv] over half h of tile i
+        const int vs = i % NV;
+        if (!mbar_wait(pfull(h, i & 1), (i >> 1) & 1)) fail = 1;
+        if (h == 0 && !mbar_wait(vfull(vs), (i / NV) & 1)) fail = 1;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t vd = umma_desc_add(dV, vs * C_::VST + h * (KT / 2) * 128);
+          const uint32_t tP = tmem + C_::t_p(i & 1, h), acc = i > 0 || h > 0 ? 1u : 0u;
 #pragma unroll
-            for (int ks = 0; ks < KT / 32; ++ks)
-              umma_bf16_ts(tmem + T_O, tP + ks * 8, umma_desc_add(vd, ks * 16 * 128), ID_PV, ks > 0 ? 1u : acc);
-            umma_commit(pvdone(h));
-            if (h == 1) umma_commit(vfree(vs));
-          }
-          __syncwarp();
-        };
-        if (NT > 0 && !mbar_wait(qready, 0)) fail = 1;
-        int ks_ = 0, kp = 0;
-        if (fold) {
-          // whole tiles: S of 128 keys, and P V once a row's both halves have their weights
-          constexpr uint32_t ID_S2 = KEYS ? umma_idesc_f16(QM, KT, 0, 0) : umma_idesc_bf16(QM, KT, 0, 0);
+          for (int ks = 0; ks < KT / 32; ++ks)
+            umma_bf16_ts(tmem + T_O, tP + ks * 8, umma_desc_add(vd, ks * 16 * 128), ID_PV, ks > 0 ? 1u : acc);
+          umma_commit(pvdone(h));
+          if (h == 1) umma_commit(vfree(vs));
+        }
+        __syncwarp();
+      };
+      if (NT > 0 && !mbar_wait(qready, 0)) fail = 1;
+      int ks_ = 0, kp = 0;
+      if (fold) {
+        // whole tiles: S of 128 keys, and P V once a row's both halves have their weights
+        constexpr uint32_t ID_S2 = KEYS ? umma_idesc_f16(QM, KT, 0, 0) : umma_idesc_bf16(QM, KT, 0, 0);
 #pragma unroll 1
-          for (int i = 0; NT > 0 && i <= NT; ++i) {
-            if (i < NT) {
-              if (!mbar_wait(KEYS ? kaready(ks_) : kfull(ks_), kp)) fail = 1;
-              if (KEYS && i > 0 && !(mbar_wait(staken(0), (i - 1) & 1) && mbar_wait(staken(1), (i - 1) & 1))) fail = 1;
-              tc_fence_after();
-              if (elect_one()) {
-                const uint64_t kd = umma_desc_add(dK, ks_ * C_::KV);
+        for (int i = 0; NT > 0 && i <= NT; ++i) {
+          if (i < NT) {
+            if (!mbar_wait(KEYS ? kaready(ks_) : kfull(ks_), kp)) fail = 1;
+            if (KEYS && i > 0 && !(mbar_wait(staken(0), (i - 1) & 1) && mbar_wait(staken(1), (i - 1) & 1))) fail = 1;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t kd = umma_desc_add(dK, ks_ * C_::KV);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                  umma_bf16_ts(tmem + C_::t_s(i & 1), tmem + T_Q + kk * 8,
-                               umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S2, kk > 0);
-                umma_commit(sfull(0, i & 1));
-                umma_commit(sfull(1, i & 1));
-                umma_commit(kfree(ks_));
-              }
-              __syncwarp();
-              if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_ts(tmem + C_::t_s(i & 1), tmem + T_Q + kk * 8,
+                             umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S2, kk > 0);
+              umma_commit(sfull(0, i & 1));
+              umma_commit(sfull(1, i & 1));
+              umma_commit(kfree(ks_));
             }
-            if (i > 0) {
-              const int j = i - 1, vs = j % NV;
-              if (!(mbar_wait(pfull(0, j & 1), (j >> 1) & 1) && mbar_wait(pfull(1, j & 1), (j >> 1) & 1))) fail = 1;
-              if (!mbar_wait(vfull(vs), (j / NV) & 1)) fail = 1;
-              tc_fence_after();
-              if (elect_one()) {
-                const uint64_t vd = umma_desc_add(dV, vs * C_::VST);
-#pragma unroll
-                for (int ks = 0; ks < KT / 16; ++ks)
-                  umma_bf16_ts(tmem + T_O, tmem + C_::t_p(j & 1, ks / 4) + (ks % 4) * 8,
-                               umma_desc_add(vd, ks * 16 * 128), ID_PV, ks > 0 || j > 0 ? 1u : 0u);
-                umma_commit(pvdone(0));
-                umma_commit(pvdone(1));
-                umma_commit(vfree(vs));
-              }
-              __syncwarp();
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int i = 0; NT > 0 && i <= NT; ++i) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              if (i < NT) {
-                if (h == 0 && !mbar_wait(KEYS ? kaready(ks_) : kfull(ks_), kp)) fail = 1;
-                if (KEYS && i > 0 && !mbar_wait(staken(h), (i - 1) & 1)) fail = 1;
-                tc_fence_after();
-                if (elect_one()) {
-                  const uint64_t kd = umma_desc_add(dK, ks_ * C_::KV + h * (KT / 2) * 128);   // keys 64 h ..
-#pragma unroll
-                  for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16_ts(tmem + C_::t_s(i & 1) + 64 * h, tmem + T_Q + kk * 8,
-                                 umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S, kk > 0);
-                  umma_commit(sfull(h, i & 1));
-                  if (h == 1) umma_commit(kfree(ks_));
-                }
-                __syncwarp();
-              }
-              if (i > 0) mma_pv(i - 1, h);
-            }
+            __syncwarp();
             if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
           }
-        }
-        if (NT > 0 && elect_one()) umma_commit(alldone);
-        __syncwarp();
-      } else if (w == W0 + 1) {
-        // ========================================================== loads
-        if (lane == 0) {
-          s_fail = 0;
-          for (int s = 0; s < 3; ++s) {
-            mbar_init(kfull(s), KEYS ? 2 : 1);   // the loads, and with a key delta the tile's anchors
-            mbar_init(kfree(s), 1);
-            mbar_init(kaready(s), 8);
-          }
-          for (int s = 0; s < 2; ++s) {
-            mbar_init(vfull(s), 1);
-            mbar_init(vfree(s), 1);
-            mbar_init(lrfull(s), 1);
-            mbar_init(lrfree(s), 1);
-            for (int b = 0; b < 2; ++b) {
-              mbar_init(sfull(s, b), 1);
-              mbar_init(pfull(s, b), fold ? 2 : 4);
+          if (i > 0) {
+            const int j = i - 1, vs = j % NV;
+            if (!(mbar_wait(pfull(0, j & 1), (j >> 1) & 1) && mbar_wait(pfull(1, j & 1), (j >> 1) & 1))) fail = 1;
+            if (!mbar_wait(vfull(vs), (j / NV) & 1)) fail = 1;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t vd = umma_desc_add(dV, vs * C_::VST);
+#pragma unroll
+              for (int ks = 0; ks < KT / 16; ++ks)
+                umma_bf16_ts(tmem + T_O, tmem + C_::t_p(j & 1, ks / 4) + (ks % 4) * 8,
+                             umma_desc_add(vd, ks * 16 * 128), ID_PV, ks > 0 || j > 0 ? 1u : 0u);
+              umma_commit(pvdone(0));
+              umma_commit(pvdone(1));
+              umma_commit(vfree(vs));
             }
-            mbar_init(staken(s), fold ? 2 : 4);
-            mbar_init(dkfull(s), 1);
-            mbar_init(dkfree(s), 4);
-            mbar_init(pvdone(s), 1);
-          }
-          mbar_init(qready, NSM);
-          mbar_init(treeready, 1);
-          mbar_init(alldone, 1);
-          fence_mbar_init();
-          for (int i = 0; i < min(NK, NT); ++i) {
-            if (KEYS && i < NL) load_lrk(i);
-            load_k(i);
-            if (i < NV) load_v(i);
+            __syncwarp();
           }
         }
-        __syncwarp();
-        setup_sync();
-        // the tree, while the first tiles are on their way; a bad one's outputs are left unwritten
-        const bool ok = tree_masks_warp(
-            tp.parent ? tp.parent + ((int64_t)seq * tp.n_trees + tree) * n : nullptr, n, m, masks);
-        if (!ok) masks[lane] = masks[lane + 32] = 0;
-        if (lane == 0) s_bad = !ok;
-        __syncwarp();
-        if (lane == 0) {
+      } else {
+#pragma unroll 1
+        for (int i = 0; NT > 0 && i <= NT; ++i) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (i < NT) {
+              if (h == 0 && !mbar_wait(KEYS ? kaready(ks_) : kfull(ks_), kp)) fail = 1;
+              if (KEYS && i > 0 && !mbar_wait(staken(h), (i - 1) & 1)) fail = 1;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t kd = umma_desc_add(dK, ks_ * C_::KV + h * (KT / 2) * 128);   // keys 64 h ..
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                  umma_bf16_ts(tmem + C_::t_s(i & 1) + 64 * h, tmem + T_Q + kk * 8,
+                               umma_desc_add(kd, (kk >> 2) * (KT * 128) + (kk & 3) * 32), ID_S, kk > 0);
+                umma_commit(sfull(h, i & 1));
+                if (h == 1) umma_commit(kfree(ks_));
+              }
+              __syncwarp();
+            }
+            if (i > 0) mma_pv(i - 1, h);
+          }
+          if (++ks_ == NK) { ks_ = 0; kp ^= 1; }
+        }
+      }
+      if (NT > 0 && elect_one()) umma_commit(alldone);
+      __syncwarp();
+    } else if (w == W0 + 1) {
+      // ========================================================== loads
+      if (lane == 0) {
+        s_fail = 0;
+        for (int s = 0; s < 3; ++s) {
+          mbar_init(kfull(s), KEYS ? 2 : 1);   // the loads, and with a key delta the tile's anchors
+          mbar_init(kfree(s), 1);
+          mbar_init(kaready(s), 8);
+        }
+        for (int s = 0; s < 2; ++s) {
+          mbar_init(vfull(s), 1);
+          mbar_init(vfree(s), 1);
+          mbar_init(lrfull(s), 1);
+          mbar_init(lrfree(s), 1);
+          for (int b = 0; b < 2; ++b) {
+            mbar_init(sfull(s, b), 1);
+            mbar_init(pfull(s, b), fold ? 2 : 4);
+          }
+          mbar_init(staken(s), fold ? 2 : 4);
+          mbar_init(dkfull(s), 1);
+          mbar_init(dkfree(s), 4);
+          mbar_init(pvdone(s), 1);
+        }
+        mbar_init(qready, NSM);
+        mbar_init(treeready, 1);
+        mbar_init(alldone, 1);
+        fence_mbar_init();
+        for (int i = 0; i < min(NK, NT); ++i) {
+          if (KEYS && i < NL) load_lrk(i);
+          load_k(i);
+          if (i < NV) load_v(i);
+        }
+      }
+      __syncwarp();
+      setup_sync();
+      // the tree, while the first tiles are on their way; a bad one's outputs are left unwritten
+      const bool ok = tree_masks_warp(
+          tp.parent ? tp.parent + ((int64_t)seq * tp.n_trees + tree) * n : nullptr, n, m, masks);
+      if (!ok) masks[lane] = masks[lane + 32] = 0;
+      if (lane == 0) s_bad = !ok;
+      __syncwarp();
+      if (lane == 0) {
         mbar_arrive(treeready);
         // refills in the order the MMAs free the stages: dK and S of tile i, then P V of tile i - 1
         for (int i = 0; i < NT; ++i) {
@@ -358,63 +370,63 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
             load_v(i - 1 + NV);
           }
         }
-        }
-      } else if (KEYS && w == W0 + 2) {
-        // ========================================================== dK
-        constexpr uint32_t ID_DK = umma_idesc_bf16(KT, 2 * FP, 0, 1);
-        constexpr uint32_t BROW = 4 * FP, BPART = R * BROW;   // bytes of a B_k row's part, and of the part
-        setup_sync();
-        const uint64_t dLRk = umma_desc(lrk_u, 16, 8 * C_::LR_ROWB, C_::LR_LAYOUT);
-        const uint64_t dBk = umma_desc(bk_u, BPART, 8 * BROW, BROW == 128 ? 2 : 4);
-        for (int i = 0; i < NT; ++i) {
-          if (!mbar_wait(lrfull(i % NL), (i / NL) & 1)) fail = 1;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            // the buffer's last part has been read: the other part's, or (two buffers) this one's
-            if (C_::NDK == 2 ? i > 0 : i + h > 0) {
-              const int o = C_::NDK == 2 ? h : 1 - h;
-              if (!mbar_wait(dkfree(o), (C_::NDK == 1 && h == 1 ? i : i - 1) & 1)) fail = 1;
-            }
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t lr = umma_desc_add(dLRk, (i % NL) * C_::LRK);
-#pragma unroll
-              for (int ks = 0; ks < R / 16; ++ks)
-                umma_bf16(tmem + T_DK + (C_::NDK == 2 ? 2 * FP * h : 0), umma_desc_add(lr, ks * 32),
-                          umma_desc_add(dBk, h * BPART + ks * 16 * BROW), ID_DK, ks > 0);
-              umma_commit(dkfull(h));
-              if (h == 1) umma_commit(lrfree(i % NL));
-            }
-            __syncwarp();
-          }
-        }
-      } else if (KEYS && w == W0 + 3) {
-        // ========================================================== anchors s R(k0)
-        // two adjacent frequencies a lane
-        const int f = 2 * lane < H2 ? 2 * lane : 0;
-        const double th0 = rt.theta[f], th1 = rt.theta[f + 1];
-        setup_sync();
-        int ks_ = 0, kp = 1;
-        for (int i = 0; i < NT; ++i) {
-          if (i >= 3 && !mbar_wait(kaready(ks_), kp)) fail = 1;   // build(i - 3) has read its slot
-          const int64_t k0 = n0 + i == Nc ? C : (int64_t)(n0 + i) * KT;
-          const float2 a = rope_cs_exact(k0, th0), b = rope_cs_exact(k0, th1);
-          if (2 * lane < H2)
-            anc[ks_ * 32 + lane] = make_uint2(h2_bits(__floats2half2_rn(a.x * p.s, b.x * p.s)),
-                                              h2_bits(__floats2half2_rn(a.y * p.s, b.y * p.s)));
-          __syncwarp();
-          if (lane == 0) mbar_arrive(kfull(ks_));
-          if (++ks_ == 3) { ks_ = 0; kp ^= 1; }
-        }
-      } else {
-        setup_sync();
       }
-      __syncwarp();
-      cluster_sync_all();
-      cluster_sync_all();
+    } else if (KEYS && w == W0 + 2) {
+      // ========================================================== dK
+      constexpr uint32_t ID_DK = umma_idesc_bf16(KT, 2 * FP, 0, 1);
+      constexpr uint32_t BROW = 4 * FP, BPART = R * BROW;   // bytes of a B_k row's part, and of the part
+      setup_sync();
+      const uint64_t dLRk = umma_desc(lrk_u, 16, 8 * C_::LR_ROWB, C_::LR_LAYOUT);
+      const uint64_t dBk = umma_desc(bk_u, BPART, 8 * BROW, BROW == 128 ? 2 : 4);
+      for (int i = 0; i < NT; ++i) {
+        if (!mbar_wait(lrfull(i % NL), (i / NL) & 1)) fail = 1;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          // the buffer's last part has been read: the other part's, or (two buffers) this one's
+          if (C_::NDK == 2 ? i > 0 : i + h > 0) {
+            const int o = C_::NDK == 2 ? h : 1 - h;
+            if (!mbar_wait(dkfree(o), (C_::NDK == 1 && h == 1 ? i : i - 1) & 1)) fail = 1;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t lr = umma_desc_add(dLRk, (i % NL) * C_::LRK);
+#pragma unroll
+            for (int ks = 0; ks < R / 16; ++ks)
+              umma_bf16(tmem + T_DK + (C_::NDK == 2 ? 2 * FP * h : 0), umma_desc_add(lr, ks * 32),
+                        umma_desc_add(dBk, h * BPART + ks * 16 * BROW), ID_DK, ks > 0);
+            umma_commit(dkfull(h));
+            if (h == 1) umma_commit(lrfree(i % NL));
+          }
+          __syncwarp();
+        }
+      }
+    } else if (KEYS && w == W0 + 3) {
+      // ========================================================== anchors s R(k0)
+      // two adjacent frequencies a lane
+      const int f = 2 * lane < H2 ? 2 * lane : 0;
+      const double th0 = rt.theta[f], th1 = rt.theta[f + 1];
+      setup_sync();
+      int ks_ = 0, kp = 1;
+      for (int i = 0; i < NT; ++i) {
+        if (i >= 3 && !mbar_wait(kaready(ks_), kp)) fail = 1;   // build(i - 3) has read its slot
+        const int64_t k0 = n0 + i == Nc ? C : (int64_t)(n0 + i) * KT;
+        const float2 a = rope_cs_exact(k0, th0), b = rope_cs_exact(k0, th1);
+        if (2 * lane < H2)
+          anc[ks_ * 32 + lane] = make_uint2(h2_bits(__floats2half2_rn(a.x * p.s, b.x * p.s)),
+                                            h2_bits(__floats2half2_rn(a.y * p.s, b.y * p.s)));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kfull(ks_));
+        if (++ks_ == 3) { ks_ = 0; kp ^= 1; }
+      }
     } else {
-      if constexpr (KEYS) regs_inc<112>();
-      if (KEYS && w >= NSM) {
+      setup_sync();
+    }
+    __syncwarp();
+    cluster_sync_all();
+    cluster_sync_all();
+  } else {
+    if constexpr (KEYS) regs_inc<112>();
+    if (KEYS && w >= NSM) {
       // ============================================================ K^a build
       // thread: key 32 sp + lane (its TMEM lane) and half h of the frequencies, in pairs
       const int key = 32 * (w & 3) + lane, h = (w - NSM) >> 2;
@@ -533,7 +545,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         const uint4 v = *reinterpret_cast<const uint4*>(Bv + (int64_t)(i / (D / 8)) * p.n_kv * D + 8 * (i % (D / 8)));
         sts128(bk_u + 16 * i, v.x, v.y, v.z, v.w);
       }
-      } else {
+    } else {
       // ============================================================ softmax
       // This thread's query row, in TMEM lane 32 sp + lane, and its half h of a tile's
       // keys: two warps share a row block, h = 0 ahead of h = 1 by about half a tile's
@@ -703,20 +715,20 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
-              const uint64_t xa2 = fma_f2(f2(__uint_as_float(sv[k][c]), __uint_as_float(sv[k][c + 1])), scl, nmu);
-              float p0, p1;
-              if (!KEYS && (c / 2) % kPolyEvery == 0) {
-                const float2 pp = f2_unpack(exp2_poly_f2(xa2));
-                p0 = pp.x;
-                p1 = pp.y;
-              } else {
-                const float2 xa = f2_unpack(xa2);
-                p0 = fast_exp2(xa.x);
-                p1 = fast_exp2(xa.y);
-              }
-              acc = add_f2(acc, f2(p0, p1));
-              pk[16 * k + c / 2] = pack_bf16(p0, p1);
+            const uint64_t xa2 = fma_f2(f2(__uint_as_float(sv[k][c]), __uint_as_float(sv[k][c + 1])), scl, nmu);
+            float p0, p1;
+            if (!KEYS && (c / 2) % kPolyEvery == 0) {
+              const float2 pp = f2_unpack(exp2_poly_f2(xa2));
+              p0 = pp.x;
+              p1 = pp.y;
+            } else {
+              const float2 xa = f2_unpack(xa2);
+              p0 = fast_exp2(xa.x);
+              p1 = fast_exp2(xa.y);
             }
+            acc = add_f2(acc, f2(p0, p1));
+            pk[16 * k + c / 2] = pack_bf16(p0, p1);
+          }
           const float2 accf = f2_unpack(acc);
           lsum += accf.x + accf.y;
           if (KEYS && i > 0) {   // P V of this half's last weights has read them
@@ -783,94 +795,94 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
           }
         }
       }
-      }
-      cluster_sync_all();
-      // ---- merge: this CTA's share of the rows, a warp a row
-      constexpr int NCH = D / 4, NW = NSM + C_::NB, NLO = R > 32 ? 2 : 1;
-      const uint32_t pol = k_u + C_::P_OL, pml = k_u + C_::P_ML;
-      const int share = (rows + S - 1) / S;
-      const int r1 = min(rows, (split + 1) * share);
-      const int c4 = lane & (NCH - 1);   // this lane's four columns
-      const int lr0 = p.r < 16 ? 8 : 0;  // r = 8: the value half sits in columns 8..15
-      // (kept short: it runs once, so every instruction of it is fetched cold)
-      // partial i of a row: CTA i / F, lane row + 64 (i mod F) (F = 2 folded; 64 is a
-      // multiple of the chunk swizzle's period)
-      const int F = fold ? 2 : 1, np = S * F;
-      if (!mbar_wait(treeready, 0)) fail = 1;
-      for (int r_ = split * share + w; r_ < r1 && !s_bad; r_ += NW) {
-        const uint32_t ml = dsmem_addr(pml + 8 * (r_ + 64 * (lane & (F - 1))), lane < np ? lane / F : 0);
-        const float mk = dsmem_ld(ml), lk = dsmem_ld(ml + 4);
-        const uint32_t oa = k_u + (uint32_t)r_ * (D * 4) + (uint32_t)(c4 ^ (r_ & (NCH - 1))) * 16;
-        const uint32_t la_ = pol + (uint32_t)(r_ * R + (lane & (R - 1))) * 4;
-        float wk = lane < np ? mk : -INFINITY, inv = 0.f;   // the partials' weights, one a lane
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lo[NLO] = {};
-#pragma unroll 1
-        for (int k0 = 0; k0 < np; k0 += 8) {
-          float4 o[8];
-          float l[8][NLO];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {   // requested before the weights are known
-            if (k0 + k >= np) break;
-            const uint32_t f = (k0 + k) & (F - 1), kc = (k0 + k) / F;
-            o[k] = dsmem_ld4(dsmem_addr(oa + f * (64 * D * 4), kc));
-#pragma unroll
-            for (int h = 0; h < NLO; ++h) l[k][h] = dsmem_ld(dsmem_addr(la_ + f * (64 * R * 4) + 128 * h, kc));
-          }
-          if (k0 == 0) {
-            float mx = wk;
-#pragma unroll
-            for (int k = kMaxSplits; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-            wk = wk == -INFINITY ? 0.f : fast_exp2(wk - mx);
-            float lt = wk == 0.f ? 0.f : wk * lk;
-#pragma unroll
-            for (int k = kMaxSplits; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
-            lt = __shfl_sync(0xffffffffu, lt, 0);
-            inv = lt > 0.f ? 1.f / lt : 0.f;
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float wv = __shfl_sync(0xffffffffu, wk, k0 + k);
-            if (wv != 0.f) {   // a split without keys leaves nothing: its words are not read as numbers
-              acc.x = fmaf(wv, o[k].x, acc.x);
-              acc.y = fmaf(wv, o[k].y, acc.y);
-              acc.z = fmaf(wv, o[k].z, acc.z);
-              acc.w = fmaf(wv, o[k].w, acc.w);
-#pragma unroll
-              for (int h = 0; h < NLO; ++h) lo[h] = fmaf(wv, l[k][h], lo[h]);
-            }
-          }
-        }
-        // O_lr B_v^a (with a key delta all rows are one agent's, its B_v in shared memory)
-        int node, ag;
-        const int64_t off = locate(r_, node, ag) + 4 * c4;
-        const int64_t ldB = KEYS ? D : (int64_t)p.n_kv * D;
-        const __nv_bfloat16* B =
-            KEYS ? reinterpret_cast<const __nv_bfloat16*>(smem + C_::OFF_BK) + 4 * c4
-                 : reinterpret_cast<const __nv_bfloat16*>(p.B_v) + (int64_t)ag * p.r * ldB + kvh * D + 4 * c4;
-        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int j = 0; j < p.r; ++j) {
-          const uint2 bw = *reinterpret_cast<const uint2*>(B + j * ldB);
-          const float2 blo = unpack_bf16(bw.x), bhi = unpack_bf16(bw.y);
-          const int jj = lr0 + j;
-          const float lv = __shfl_sync(0xffffffffu, NLO > 1 && jj >= 32 ? lo[NLO - 1] : lo[0], jj & 31);
-          z.x = fmaf(lv, blo.x, z.x);
-          z.y = fmaf(lv, blo.y, z.y);
-          z.z = fmaf(lv, bhi.x, z.z);
-          z.w = fmaf(lv, bhi.y, z.w);
-        }
-        if (lane >= NCH) continue;
-        const float4 o = make_float4(fmaf(p.s, z.x, acc.x) * inv, fmaf(p.s, z.y, acc.y) * inv,
-                                     fmaf(p.s, z.z, acc.z) * inv, fmaf(p.s, z.w, acc.w) * inv);
-        if (p.out_bf16)
-          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + off) =
-              make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-        else
-          *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + off) = o;
-      }
-      cluster_sync_all();   // the partials are read before any CTA of the cluster exits
     }
+    cluster_sync_all();
+    // ---- merge: this CTA's share of the rows, a warp a row
+    constexpr int NCH = D / 4, NW = NSM + C_::NB, NLO = R > 32 ? 2 : 1;
+    const uint32_t pol = k_u + C_::P_OL, pml = k_u + C_::P_ML;
+    const int share = (rows + S - 1) / S;
+    const int r1 = min(rows, (split + 1) * share);
+    const int c4 = lane & (NCH - 1);   // this lane's four columns
+    const int lr0 = p.r < 16 ? 8 : 0;  // r = 8: the value half sits in columns 8..15
+    // (kept short: it runs once, so every instruction of it is fetched cold)
+    // partial i of a row: CTA i / F, lane row + 64 (i mod F) (F = 2 folded; 64 is a
+    // multiple of the chunk swizzle's period)
+    const int F = fold ? 2 : 1, np = S * F;
+    if (!mbar_wait(treeready, 0)) fail = 1;
+    for (int r_ = split * share + w; r_ < r1 && !s_bad; r_ += NW) {
+      const uint32_t ml = dsmem_addr(pml + 8 * (r_ + 64 * (lane & (F - 1))), lane < np ? lane / F : 0);
+      const float mk = dsmem_ld(ml), lk = dsmem_ld(ml + 4);
+      const uint32_t oa = k_u + (uint32_t)r_ * (D * 4) + (uint32_t)(c4 ^ (r_ & (NCH - 1))) * 16;
+      const uint32_t la_ = pol + (uint32_t)(r_ * R + (lane & (R - 1))) * 4;
+      float wk = lane < np ? mk : -INFINITY, inv = 0.f;   // the partials' weights, one a lane
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float lo[NLO] = {};
+#pragma unroll 1
+      for (int k0 = 0; k0 < np; k0 += 8) {
+        float4 o[8];
+        float l[8][NLO];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {   // requested before the weights are known
+          if (k0 + k >= np) break;
+          const uint32_t f = (k0 + k) & (F - 1), kc = (k0 + k) / F;
+          o[k] = dsmem_ld4(dsmem_addr(oa + f * (64 * D * 4), kc));
+#pragma unroll
+          for (int h = 0; h < NLO; ++h) l[k][h] = dsmem_ld(dsmem_addr(la_ + f * (64 * R * 4) + 128 * h, kc));
+        }
+        if (k0 == 0) {
+          float mx = wk;
+#pragma unroll
+          for (int k = kMaxSplits; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+          wk = wk == -INFINITY ? 0.f : fast_exp2(wk - mx);
+          float lt = wk == 0.f ? 0.f : wk * lk;
+#pragma unroll
+          for (int k = kMaxSplits; k > 0; k >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, k);
+          lt = __shfl_sync(0xffffffffu, lt, 0);
+          inv = lt > 0.f ? 1.f / lt : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float wv = __shfl_sync(0xffffffffu, wk, k0 + k);
+          if (wv != 0.f) {   // a split without keys leaves nothing: its words are not read as numbers
+            acc.x = fmaf(wv, o[k].x, acc.x);
+            acc.y = fmaf(wv, o[k].y, acc.y);
+            acc.z = fmaf(wv, o[k].z, acc.z);
+            acc.w = fmaf(wv, o[k].w, acc.w);
+#pragma unroll
+            for (int h = 0; h < NLO; ++h) lo[h] = fmaf(wv, l[k][h], lo[h]);
+          }
+        }
+      }
+      // O_lr B_v^a (with a key delta all rows are one agent's, its B_v in shared memory)
+      int node, ag;
+      const int64_t off = locate(r_, node, ag) + 4 * c4;
+      const int64_t ldB = KEYS ? D : (int64_t)p.n_kv * D;
+      const __nv_bfloat16* B =
+          KEYS ? reinterpret_cast<const __nv_bfloat16*>(smem + C_::OFF_BK) + 4 * c4
+               : reinterpret_cast<const __nv_bfloat16*>(p.B_v) + (int64_t)ag * p.r * ldB + kvh * D + 4 * c4;
+      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int j = 0; j < p.r; ++j) {
+        const uint2 bw = *reinterpret_cast<const uint2*>(B + j * ldB);
+        const float2 blo = unpack_bf16(bw.x), bhi = unpack_bf16(bw.y);
+        const int jj = lr0 + j;
+        const float lv = __shfl_sync(0xffffffffu, NLO > 1 && jj >= 32 ? lo[NLO - 1] : lo[0], jj & 31);
+        z.x = fmaf(lv, blo.x, z.x);
+        z.y = fmaf(lv, blo.y, z.y);
+        z.z = fmaf(lv, bhi.x, z.z);
+        z.w = fmaf(lv, bhi.y, z.w);
+      }
+      if (lane >= NCH) continue;
+      const float4 o = make_float4(fmaf(p.s, z.x, acc.x) * inv, fmaf(p.s, z.y, acc.y) * inv,
+                                   fmaf(p.s, z.z, acc.z) * inv, fmaf(p.s, z.w, acc.w) * inv);
+      if (p.out_bf16)
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + off) =
+            make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+      else
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + off) = o;
+    }
+    cluster_sync_all();   // the partials are read before any CTA of the cluster exits
+  }
   if (fail) s_fail = 1;
   tc_fence_before();
   __syncthreads();
