@@ -453,10 +453,9 @@ typedef struct {
  * the caches.  Cache rows no node sees may hold anything, NaN included; the
  * rows of a tree's own nodes must be finite.  Outputs of nodes at or past
  * tree_len are left as they were.
- * On the tensor cores (bf16, head_dim 128) the scores take queries and keys in
- * fp16 as lora_attn_prefill does (below 65504 in magnitude), except with B_k
- * NULL, where they stay bf16.  No workspace: the key splits of a block are a
- * thread-block cluster.
+ * With bf16 inputs the scores take queries and keys in fp16 as lora_attn_prefill
+ * does (below 65504 in magnitude), except with B_k NULL, where they stay bf16.
+ * No workspace: the key splits of a block are a thread-block cluster.
  * Errors: as lora_attn_prefill; LA_ERR_INVALID_ARG for a null tree, n_trees
  * neither 1 nor n_agents or n outside [1, LA_TREE_MAX_NODES];
  * LA_ERR_CAPACITY (max_kv_len > L_max or < n_trees * n); LA_ERR_UNSUPPORTED

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
   float* xref = reinterpret_cast<float*>(misc + 1536);   // a row's reference maximum, handed between its two warps
   float* xsum = xref + QM;
   uint64_t* masks = reinterpret_cast<uint64_t*>(misc + 2560);
-  const uint32_t b0 = smem_u32(misc + 3072);
+  const uint32_t b0 = smem_u32(masks + kTreeMaxNodes);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 3584);
   float* thf = reinterpret_cast<float*>(misc + 3600);
   __shared__ int s_bad, s_fail;

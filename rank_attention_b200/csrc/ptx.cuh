@@ -41,23 +41,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int lim
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
-// The same for kernels with many waiting warps: a poll that finds the phase
-// open sleeps until it completes or 20 us have passed, instead of polling again
-// and again beside the working warps (at most 2^18 polls, about 5 s).
-__device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity) {
-#pragma unroll 1
-  for (int i = 0; i < (1 << 18); ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
-}
 // Orders this thread's generic-proxy shared-memory writes before later
 // async-proxy (TMA) accesses of the same memory.
 __device__ __forceinline__ void fence_proxy_async_smem() {
