@@ -156,3 +156,27 @@ def test_graph_with_changing_segments(la):
         ref = O.grouped_delta(x, A, B, y, start, agent, 2.0)
         ref[start[-1]:] = 0
         assert np.abs(to_np(out) - ref).max() <= 2.0 ** -8 * np.abs(ref).max() + 1e-3
+
+
+def test_two_streams_at_once_and_one_agent_expanded(la):
+    gen = torch.Generator().manual_seed(5)
+    f = lambda *s, std=1.0: (torch.randn(*s, generator=gen) * std).to(torch.bfloat16).to(DEV)  # noqa: E731
+    runs = []
+    for T, H, N, r, start, agent in ((700, 512, 256, 32, [0, 300, 700], [0, 1]), (90, 1024, 512, 16, [0, 1, 90], [1, 0])):
+        x, y, A, B = f(T, H), f(T, N), f(H, r, std=0.05), f(2, r, N, std=0.05)
+        out = torch.zeros_like(y)
+        ss, sa = (torch.tensor(v, dtype=torch.int32, device=DEV) for v in (start, agent))
+        args = la.make_grouped_args(x, A.expand(2, H, r), B, y, out, ss, sa, lora_scale=2.0)   # stride 0: one A
+        runs.append((torch.cuda.Stream(), args, (x, A, B, y, start, agent), out, (ss, sa)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, args, *_rest in runs:
+            with torch.cuda.stream(s):
+                la.lora_grouped_delta(args)
+    torch.cuda.synchronize()
+    for s, args, (x, A, B, y, start, agent), out, keep in runs:
+        ref = O.grouped_delta(x.cpu(), A.cpu(), B.cpu(), to_np(y), start, agent, 2.0)
+        mag = O.grouped_delta(x.abs().cpu(), A.abs().cpu(), B.abs().cpu(), 0 * to_np(y), start, agent, 2.0)
+        tol = 2.0 ** -8 * np.abs(ref) + mag * ((x.shape[1] + B.shape[1] + 8) * 2.0 ** -24 + 2.0 ** -16) + \
+            2.0 ** -24 * np.abs(to_np(y))
+        assert (np.abs(to_np(out) - ref) <= tol).all()

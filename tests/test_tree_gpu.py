@@ -312,3 +312,69 @@ def test_offsets_past_32_bits(la):
     la.lora_attn_tree(args, la.make_tree_args(par))
     torch.cuda.synchronize()
     check(la, i, out, torch.bfloat16)
+
+
+def test_wide_group_own_lr_without_key_delta_and_chains_of_every_agent(la):
+    run(la, S=1, A=1, kv=1, g=64, ctx=(150,), n=3, seed=15)                          # 192 rows: two blocks
+    run(la, S=1, A=1, kv=1, g=64, d=64, ctx=(20,), n=64, keys=False, seed=16)        # 32 blocks
+    run(la, S=2, A=3, ctx=(259, 77), n=6, lr_agents=True, keys=False, seed=17)
+    run(la, S=1, A=2, r=8, ctx=(140,), n=20, per_agent=True, lr_agents=True, keys=False, d=64, seed=18)
+    run(la, dtype=torch.float32, out_dtype=torch.bfloat16, ctx=(130,), n=5, seed=19)
+    for dt in (torch.bfloat16, torch.float32):   # neither parents nor lengths: a chain an agent
+        i = make(dtype=dt, A=3, ctx=(201,), n=7, per_agent=True, garbage=False, seed=20)
+        i["parent"] = None
+        args, tree, out, keep = launch(la, i, dt)
+        la.lora_attn_tree(args, tree)
+        torch.cuda.synchronize()
+        check(la, i, out, dt)
+
+
+def test_two_streams_at_once(la):
+    """Nothing is shared between calls: two of different shapes in flight together."""
+    cases = [make(S=2, A=3, ctx=(1500, 900), n=8, garbage=False, seed=21),
+             make(S=1, A=2, r=32, ctx=(2100,), n=40, per_agent=True, garbage=False, seed=22)]
+    runs = [(torch.cuda.Stream(), *launch(la, i)) for i in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, args, tree, out, keep in runs:
+            with torch.cuda.stream(s):
+                la.lora_attn_tree(args, tree)
+    torch.cuda.synchronize()
+    for i, (s, args, tree, out, keep) in zip(cases, runs):
+        check(la, i, out, torch.bfloat16)
+
+
+FIRST_IN_CAPTURE = """
+import torch
+from tests import test_tree_gpu as T
+from rank_attention_b200 import lora_attn as la
+i = T.make(ctx=(300,), n=5, garbage=False, seed=23)
+args, tree, out, keep = T.launch(la, i)
+x, y = torch.randn(40, 128, device="cuda").bfloat16(), torch.randn(40, 64, device="cuda").bfloat16()
+A, B = torch.randn(128, 16, device="cuda").bfloat16(), torch.randn(2, 16, 64, device="cuda").bfloat16()
+o = torch.zeros_like(y)
+ss, sa = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 9, 40], [1, 0]))
+ga = la.make_grouped_args(x, A, B, y, o, ss, sa, lora_scale=1.0)
+q = torch.randn(1, 2, 5, 8, 128, device="cuda").bfloat16()
+qo, kl = torch.zeros_like(q), torch.tensor([7], dtype=torch.int32, device="cuda")
+qa = la.make_qk_args(q, None, None, None, None, qo, None, None, kl, rope_base=1e4, max_kv_len=20)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    la.lora_attn_tree(args, tree)
+    la.lora_grouped_delta(ga)
+    la.lora_qk_norm_rope(qa)
+g.replay()
+torch.cuda.synchronize()
+T.check(la, i, out, torch.bfloat16)
+assert (o != 0).any() and (qo != 0).any() and la.la_device_check() == 0
+print("captured")
+"""
+
+
+def test_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
