@@ -286,7 +286,10 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
     B_k may be None for lora_attn_tree alone (keys without a low-rank part).
     Sequence-sharded decode: key_pos0 is the position of the caches' key row 0;
     row_stats a float32 [n_seqs, n_agents, n_q, 2] tensor the decode fills
-    with each row's (M, L) for lora_attn_decode_combine."""
+    with each row's (M, L) for lora_attn_decode_combine.
+    The struct holds addresses; it keeps the tensors alive as long as it lives itself
+    (every make_* struct does)."""
+    keep = (k_base, v_base, lr, B_k, B_v, q, out, kv_len, row_stats)
     n_seqs, n_kv, L_max, d = k_base.shape
     n_agents, n_tok, n_q = q.shape[1], q.shape[2], q.shape[3]
     per_agent = lr.dim() == 4
@@ -325,6 +328,7 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
         assert row_stats.numel() == 2 * n_seqs * n_agents * n_q
     a.row_stats = row_stats.data_ptr() if row_stats is not None else None
     a.device = q.device.index
+    a.keep = keep
     return a
 
 
@@ -473,6 +477,7 @@ def make_tree_args(parent: Optional[torch.Tensor], tree_len: Optional[torch.Tens
     a.n_seqs = None if shape is None else shape[0]
     a.n = None if parent is None else parent.shape[2]
     a.device = None if shape is None else _same_device((parent, tree_len))
+    a.keep = (parent, tree_len)
     return a
 
 
@@ -563,7 +568,8 @@ def make_qk_args(q, k, v, w_q, w_k, q_out, k_base, v_base, kv_len, *, rope_base:
     if kv_len.dtype != torch.int32 or kv_len.shape != (n_seqs,) or not kv_len.is_contiguous():
         raise ValueError("kv_len must be int32 [n_seqs]")
     a.kv_len, a.max_kv_len, a.dtype = kv_len.data_ptr(), max_kv_len, _dt(ref)
-    a.device = _same_device((q, k, v, w_q, w_k, q_out, k_base, v_base, kv_len))
+    a.keep = (q, k, v, w_q, w_k, q_out, k_base, v_base, kv_len)
+    a.device = _same_device(a.keep)
     return a
 
 
@@ -612,7 +618,8 @@ def make_grouped_args(x, A, B, y, out, seg_start, seg_agent, *, lora_scale: floa
     a.y, a.ldy = y.data_ptr(), y.stride(0) if T > 1 else N
     a.out, a.ldo = out.data_ptr(), out.stride(0) if T > 1 else N
     a.seg_start, a.seg_agent, a.dtype = seg_start.data_ptr(), seg_agent.data_ptr(), _dt(x)
-    a.device = _same_device((x, A, B, y, out, seg_start, seg_agent))
+    a.keep = (x, A, B, y, out, seg_start, seg_agent)
+    a.device = _same_device(a.keep)
     return a
 
 
