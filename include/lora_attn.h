@@ -474,7 +474,8 @@ typedef struct {
    * s*q_seq_stride + a*q_agent_stride + j*q_tok_stride + h*d + c.  NULL: none. */
   const void* q;
   int64_t q_seq_stride, q_agent_stride, q_tok_stride;
-  void* q_out;          /* [n_seqs][n_agents][n_tokens][n_q_heads][d]; may be q itself */
+  void* q_out;          /* [n_seqs][n_agents][n_tokens][n_q_heads][d]; q itself (if q's strides are
+                           these, extents of one aside), or no overlap with any input */
   /* The new tokens' base keys and values, element (s, t, j, h, c) at
    * s*kv_in_seq_stride + t*kv_in_tree_stride + j*kv_in_tok_stride + h*d + c,
    * t < n_trees.  k NULL: only queries; v NULL: no value rows. */

@@ -274,6 +274,12 @@ extern "C" la_status lora_qk_norm_rope(const la_qk_args* a, const la_tree_args* 
     if (!stride_ok(a->q_seq_stride) || !stride_ok(a->q_agent_stride) || !stride_ok(a->q_tok_stride) ||
         a->q_tok_stride < a->n_q_heads * d)
       return LA_ERR_INVALID_ARG;
+    // q_out is dense: over a strided q its rows would land on rows not read yet
+    const int64_t tok = a->n_q_heads * d, agent = a->n_tokens * tok, seq = a->n_agents * agent;
+    if (a->q == a->q_out && a->n_tokens > 0 &&
+        ((a->n_tokens > 1 && a->q_tok_stride != tok) || (a->n_agents > 1 && a->q_agent_stride != agent) ||
+         (a->n_seqs > 1 && a->q_seq_stride != seq)))
+      return LA_ERR_INVALID_ARG;
   }
   if (a->k) {
     if (!aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->w_k, 16) || !aligned(a->k_base, 16) ||

@@ -1,0 +1,35 @@
+"""More refusals of the drafted-tree operators, before any launch: every call carries
+at least one invalid argument (no GPU needed; the addresses are never dereferenced)."""
+import ctypes
+
+import pytest
+
+from rank_attention_b200 import lora_attn as la
+from tests.test_tree_host import BAD, FAKE, UNS, grouped, qk
+
+OTHER = FAKE + 0x10000
+
+
+def norm(**kw):
+    """The status of a call with 4 query heads of 64, 2 agents, 4 tokens and 2 sequences
+    whose max_kv_len lies beyond L_max: strides that pass end there, nothing launches."""
+    return la.lib.lora_qk_norm_rope(ctypes.byref(qk(max_kv_len=257, **kw)), None, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q_out=FAKE), la.LA_ERR_CAPACITY),                                  # dense
+    (dict(q_out=FAKE, q_tok_stride=512, q_agent_stride=2048, q_seq_stride=4096), BAD),   # a fused projection's slice
+    (dict(q_out=FAKE, q_agent_stride=2048, q_seq_stride=4096), BAD),
+    (dict(q_out=FAKE, q_seq_stride=4096), BAD),
+    (dict(q_out=FAKE, q_agent_stride=0), BAD),
+    # a stride whose extent is one is not used
+    (dict(q_out=FAKE, n_seqs=1, q_seq_stride=4096), la.LA_ERR_CAPACITY),
+    (dict(q_out=FAKE, n_agents=1, q_agent_stride=4096, q_seq_stride=1024), la.LA_ERR_CAPACITY),
+    (dict(q_out=FAKE, n_tokens=1, q_tok_stride=512, q_agent_stride=256, q_seq_stride=512), la.LA_ERR_CAPACITY),
+    # another buffer: strides as before
+    (dict(q_out=OTHER, q_tok_stride=512, q_agent_stride=2048, q_seq_stride=4096), la.LA_ERR_CAPACITY),
+])
+def test_queries_in_place_must_be_dense(kw, status):
+    """q_out is written densely: over a strided q, a head's row would land on rows that
+    another block has yet to read, or on its neighbours' columns."""
+    assert norm(**kw) == status
