@@ -26,6 +26,18 @@ struct GroupedParams {
   int* err;
 };
 
+// Rows per tile: bf16 (tensor cores); fp32 where segments have 64 rows on average (their
+// sizes are known only on the device), and fp32 otherwise
+constexpr int kRowsTC = 128, kRowsWide = 64, kRowsNarrow = 16;
+inline int grouped_tile_rows(bool bf16, int n_tokens, int n_segs) {
+  if (bf16) return kRowsTC;
+  return n_tokens >= (int64_t)kRowsWide * n_segs ? kRowsWide : kRowsNarrow;
+}
+// Tiles a launch has to offer: every segment ends in at most one short tile
+inline int64_t grouped_tiles(int n_tokens, int n_segs, int rows) {
+  return ((int64_t)n_tokens + rows - 1) / rows + n_segs;
+}
+
 // One row tile of a segment.  rows == 0: no such tile.
 struct SegTile {
   int row0, rows, agent, bad;

@@ -33,7 +33,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int GM = 128;         // rows per tile
+constexpr int GM = kRowsTC;     // rows per tile
 constexpr int GC = 64;          // columns per chunk (128-byte swizzled rows)
 constexpr int GBOX = 32;        // rows per TMA box
 constexpr int GNTH = 192;
@@ -383,8 +383,7 @@ cudaError_t launch_gt(const GroupedParams& p, cudaStream_t st) {
   using C = GCfg<R>;
   CUtensorMap mx, ma, my, mb;
   if (!grouped_maps(p, R, &mx, &ma, &my, &mb)) return cudaErrorInvalidValue;
-  // every segment ends in at most one short tile
-  const int64_t tiles = (int64_t)(p.n_tokens + GM - 1) / GM + p.n_segs;
+  const int64_t tiles = grouped_tiles(p.n_tokens, p.n_segs, GM);
   // CTAs a tile: eight or four while one CTA an SM covers the launch, two while two do.
   // The sum over distributed shared memory grows with CS: 16384 tokens, r 64, 132 tiles
   // at CS 1 / 2 / 4 / 8: 90 / 77 / 99 / 203 us; 1501 tokens, r 32, 21 tiles: 42 / 25 /

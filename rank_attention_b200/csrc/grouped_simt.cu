@@ -15,7 +15,7 @@
 namespace la {
 namespace {
 
-constexpr int TM = 16, NTH = 256, KC = 64;
+constexpr int TM = kRowsNarrow, NTH = 256, KC = 64;
 constexpr int CS = 4;
 
 __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p) {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(NTH) grouped_simt_kernel(const GroupedParams p
 // products as register tiles of 4 x 4 (16 FMAs for two 16-byte shared-memory reads).
 // 2048 tokens in 8 segments, hidden and out 4096, r 64: 120 us (18 TFLOP/s), with the
 // 16-row tiles 320 us; r 16 (a quarter of the threads has ranks): 83 against 167 us.
-constexpr int WM = 64, WK = 32, WN = 64;
+constexpr int WM = kRowsWide, WK = 32, WN = 64;
 
 // acc[4][4] += rows of a (4 ty ..) x columns of b (4 tx ..) over n steps
 template <int LA, int LB>
@@ -250,12 +250,9 @@ __global__ void __launch_bounds__(NTH) grouped_wide_kernel(const GroupedParams p
 }
 
 cudaError_t launch_grouped_simt(const GroupedParams& p, cudaStream_t st) {
-  // 64-row tiles where segments have 64 rows on average (their sizes are known only
-  // on the device), else 16-row ones
-  const bool wide = p.n_tokens >= (int64_t)WM * p.n_segs;
-  const int tm = wide ? WM : TM;
-  // every segment ends in at most one short tile
-  const int64_t tiles = (int64_t)(p.n_tokens + tm - 1) / tm + p.n_segs;
+  const int tm = grouped_tile_rows(false, p.n_tokens, p.n_segs);
+  const bool wide = tm == WM;
+  const int64_t tiles = grouped_tiles(p.n_tokens, p.n_segs, tm);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CS, (unsigned)tiles, 1);
   cfg.blockDim = dim3(NTH);
@@ -298,7 +295,8 @@ extern "C" la_status lora_grouped_delta(const la_grouped_args* a, la_stream_t st
   if (a->a_agent_stride != 0 &&
       (a->a_agent_stride < (int64_t)a->hidden * a->r || (a->a_agent_stride * es) % 16 != 0))
     return LA_ERR_INVALID_ARG;
-  if ((int64_t)(a->n_tokens + 15) / 16 + a->n_segs > 65535) return LA_ERR_UNSUPPORTED;
+  const int rows = grouped_tile_rows(a->dtype == LA_BF16, a->n_tokens, a->n_segs);
+  if (grouped_tiles(a->n_tokens, a->n_segs, rows) > 65535) return LA_ERR_UNSUPPORTED;   // the grid's y
   GroupedParams p = {};
   p.x = a->x; p.ldx = a->ldx;
   p.y = a->y; p.ldy = a->ldy;

@@ -1,0 +1,45 @@
+"""Calls of the drafted-tree operators that their documentation allows and no other test
+makes, against the fp64 oracle within the operators' own bounds."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import impl as O
+from tests.helpers import to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def la():
+    from rank_attention_b200 import lora_attn
+    return lora_attn
+
+
+def grouped_tol(ref, mag, y, hidden, r, bf):
+    """The bound of the grouped products' own tests."""
+    return (2.0 ** -8 if bf else 2.0 ** -24) * np.abs(ref) + \
+        mag * ((hidden + r + 8) * 2.0 ** -24 + (2.0 ** -16 if bf else 0)) + 2.0 ** -24 * np.abs(y)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_grouped_over_a_million_tokens(la, dtype):
+    """More tokens than 65535 tiles of 16 rows: the kernel's own tile height counts."""
+    T, H, N, r = 1100003, 64, 64, 8
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    f = lambda *s, std=1.0: (torch.randn(*s, generator=gen, device=DEV) * std).to(dtype)  # noqa: E731
+    x, y, A, B = f(T, H), f(T, N), f(2, H, r, std=0.05), f(2, r, N, std=0.05)
+    out = torch.zeros_like(y)
+    cuts, who = [0, 70001, T - 1], [1, 0]
+    ss, sa = (torch.tensor(v, dtype=torch.int32, device=DEV) for v in (cuts, who))
+    la.lora_grouped_delta(la.make_grouped_args(x, A, B, y, out, ss, sa, lora_scale=2.0))
+    torch.cuda.synchronize()
+    assert la.la_device_check() == la.LA_OK
+    for lo, hi, a in ((0, 200, 1), (69900, 70001, 1), (70001, 70200, 0), (1048500, 1048700, 0), (T - 300, T - 1, 0)):
+        xs, ys = x[lo:hi].cpu(), to_np(y[lo:hi])
+        ref = O.grouped_delta(xs, A.cpu(), B.cpu(), ys, [0, hi - lo], [a], 2.0)
+        mag = O.grouped_delta(xs.abs(), A.abs().cpu(), B.abs().cpu(), 0 * ys, [0, hi - lo], [a], 2.0)
+        err = np.abs(to_np(out[lo:hi]) - ref)
+        assert (err <= grouped_tol(ref, mag, ys, H, r, dtype == torch.bfloat16)).all(), (lo, a)
+    assert (out[T - 1] == 0).all(), "the row in no segment was written"

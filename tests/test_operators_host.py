@@ -33,3 +33,14 @@ def test_queries_in_place_must_be_dense(kw, status):
     """q_out is written densely: over a strided q, a head's row would land on rows that
     another block has yet to read, or on its neighbours' columns."""
     assert norm(**kw) == status
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n_tokens=(1 << 31) - 1, dtype=la.LA_BF16), dict(n_tokens=(1 << 31) - 1, dtype=la.LA_F32),
+    dict(n_tokens=(1 << 31) - 1, n_segs=(1 << 31) - 1),
+    # one tile more than the grid holds: 128 rows a tile in bf16, 64 in fp32 (16 where segments are short)
+    dict(n_tokens=65533 * 128 + 1, dtype=la.LA_BF16), dict(n_tokens=65533 * 64 + 1, dtype=la.LA_F32),
+    dict(n_tokens=16 * 32768 + 1, n_segs=32767, dtype=la.LA_F32),
+])
+def test_grouped_refuses_more_tiles_than_the_grid_holds(kw):
+    assert la.lib.lora_grouped_delta(ctypes.byref(grouped(**kw)), None) == UNS
