@@ -191,6 +191,7 @@ struct TCfgA {
   static constexpr int RED = TM2 * CP * 4;
   static constexpr int AREA = NSTAGE2 * STAGE > RED ? NSTAGE2 * STAGE : align1k(RED);
   static constexpr size_t smem = 1024 + AREA + 128;
+  static_assert(smem >= kSmemSomeTmem && C <= 256, "kept apart from kernels with all of TMEM");
 };
 
 template <int R>

@@ -725,7 +725,7 @@ struct TCfg {
   // LR tile: rows of 2r bf16 in boxes of min(2r, 64); its swizzle span
   static constexpr int LR_ROWB = (2 * R < 64 ? 2 * R : 64) * 2;
   static constexpr uint32_t LR_LAYOUT = LR_ROWB == 128 ? 2u : (LR_ROWB == 64 ? 4u : 6u);
-  static size_t smem(int n_agents) {  // n_agents: the agents of one CTA
+  static constexpr size_t smem(int n_agents) {  // n_agents: the agents of one CTA
     return 1024 + AREA + 2 * P_TILE + align1k(SMALL) + QU_BYTES + 2 * QP_BYTES +
            (size_t)align1k(BK_BYTES) * n_agents + 128;
   }
@@ -1800,6 +1800,7 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
+  static_assert(TC_COLS < 512 || C::smem(1) >= kSmemAllTmem, "kept apart from other kernels with TMEM");
   const size_t sm = C::smem(p.agent_group);
   auto kern = decode_tc_kernel<D, R, NT, PA>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);

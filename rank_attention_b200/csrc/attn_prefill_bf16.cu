@@ -82,6 +82,7 @@ struct PCfg {
   // 18 mbarriers, the TMEM slot
   static constexpr int MISC = 1024 + 2048 + 512 + 144 + 16;
   static constexpr size_t SMEM = 1024 + OFF_MISC + MISC;
+  static_assert(SMEM >= kSmemAllTmem, "kept apart from other kernels with TMEM");
 };
 
 template <int R, int KS, bool VT>

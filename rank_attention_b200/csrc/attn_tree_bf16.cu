@@ -80,14 +80,15 @@ struct TCfg {
   // misc: anchors [3][64] float2, references and sums of the rows [2][128] float, masks [64] u64, 64 mbarriers,
   // the TMEM slot, theta [64] float
   static constexpr int MISC = 1536 + 1024 + 512 + 512 + 16 + 256;
-  // at least more than half an SM's, so that one CTA is resident: two would wait
-  // for each other's TMEM across clusters
+  // all of TMEM: one CTA an SM, and none of another kernel that holds some (at d = 64
+  // the stages alone would leave room for one)
   static constexpr int NEED = 1024 + OFF_MISC + MISC;
-  static constexpr int SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
+  static constexpr int SMEM = NEED > kSmemAllTmem ? NEED : kSmemAllTmem;
   // the partial (O, O_lr, m and l) over the drained stages
   static constexpr int P_OL = QM * D * 4, P_ML = P_OL + QM * R * 4;
   static_assert(P_ML + QM * 8 <= OFF_LRK, "the partial lies over the stages");
   static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+  static_assert(T_COLS < 512 || SMEM >= kSmemAllTmem, "kept apart from other kernels with TMEM");
   // score buffers
   __host__ __device__ static constexpr int t_s(int b) { return KEYS ? 128 : 64 + 128 * b; }
   // weights of a tile's half h (64 keys, 32 columns); without a key delta over that half's scores

@@ -14,6 +14,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int align1k(int x) { return (x + 1023) / 1024 * 1024; }
 
+// Shared memory that keeps kernels with TMEM apart.  A CTA that has allocated TMEM and
+// waits for its cluster holds its columns meanwhile.  If two such kernels (of two
+// streams) shared SMs and one of them needs all 512 columns, a CTA of each could hold
+// what the other's peer waits for, and neither tcgen05.alloc nor a cluster barrier gives
+// up.  So a kernel that takes all columns asks for at least kSmemAllTmem and any other
+// that allocates for at least kSmemSomeTmem (at most 256 columns): together they exceed
+// an SM's 228 KB (1 KB of it reserved a CTA), and so do three of the second kind.
+constexpr int kSmemSM = 228 * 1024, kSmemReserved = 1024;
+constexpr int kSmemSomeTmem = 80 * 1024;
+constexpr int kSmemAllTmem = kSmemSM - 2 * kSmemReserved - kSmemSomeTmem + 1024;
+static_assert(3 * (kSmemSomeTmem + kSmemReserved) > kSmemSM, "two CTAs of at most 256 columns");
+
 // RoPE frequencies theta_i = base^(-2i/d), formed in fp64 on the host
 struct RopeTheta {
   double theta[64];

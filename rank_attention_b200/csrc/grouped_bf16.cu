@@ -399,8 +399,9 @@ cudaError_t launch_gt(const GroupedParams& p, cudaStream_t st) {
   const int rest = 1024 + (CS > 1 ? C::RED : 0) + C::MISC;
   int ns = (113 * 1024 - rest) / C::STAGE;
   if (ns > kMaxStages) ns = kMaxStages;
-  // never three CTAs an SM: their TMEM would not fit
-  const int smem = max(rest + ns * C::STAGE, 80 * 1024);
+  // never three CTAs an SM (their TMEM would not fit), and none beside a kernel with all of it
+  static_assert(G_COLS <= 256, "TMEM of the kernels that take kSmemSomeTmem");
+  const int smem = max(rest + ns * C::STAGE, kSmemSomeTmem);
   const auto kern = grouped_tc_kernel<R>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

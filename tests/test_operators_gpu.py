@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from oracle import impl as O
+from tests import test_tree_gpu as T
 from tests.helpers import to_np
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +44,37 @@ def test_grouped_over_a_million_tokens(la, dtype):
         err = np.abs(to_np(out[lo:hi]) - ref)
         assert (err <= grouped_tol(ref, mag, ys, H, r, dtype == torch.bfloat16)).all(), (lo, a)
     assert (out[T - 1] == 0).all(), "the row in no segment was written"
+
+
+@pytest.mark.parametrize("keys", [True, False])
+def test_kernels_with_tensor_memory_on_streams_of_their_own(la, keys):
+    """Trees of head_dim 64 (all TMEM columns), grouped products and LR appends (some of
+    them), each a grid of clusters, in flight together: the same bits as alone."""
+    i = T.make(S=4, A=3, kv=4, d=64, r=16, ctx=(1500, 900, 2048, 30), n=9, per_agent=True, keys=keys, garbage=False, seed=31)
+    args, tree, out, keep = T.launch(la, i)
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    f = lambda *s, std=1.0: (torch.randn(*s, generator=gen, device=DEV) * std).to(torch.bfloat16)  # noqa: E731
+    x, y, A, B = f(3000, 2048), f(3000, 1024), f(3, 2048, 64, std=0.05), f(3, 64, 1024, std=0.05)
+    o = torch.zeros_like(y)
+    ss, sa = (torch.tensor(v, dtype=torch.int32, device=DEV) for v in ([0, 700, 1600, 3000], [2, 0, 1]))
+    ga = la.make_grouped_args(x, A, B, y, o, ss, sa, lora_scale=2.0)
+    X, A_kv, lr = f(2, 700, 2048), f(2048, 64, std=0.02), torch.zeros(2, 800, 64, dtype=torch.bfloat16, device=DEV)
+    calls = [(lambda: la.lora_attn_tree(args, tree), out), (lambda: la.lora_grouped_delta(ga), o),
+             (lambda: la.lr_cache_append(X, A_kv, lr, 17), lr)]
+    alone = []
+    for call, res in calls:
+        call()
+        torch.cuda.synchronize()
+        alone.append(res.clone())
+        res.zero_()
+    T.check(la, i, alone[0], torch.bfloat16)
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (call, _) in zip(streams, calls):
+            with torch.cuda.stream(s):
+                call()
+    torch.cuda.synchronize()
+    assert la.la_device_check() == la.LA_OK
+    for (_, res), ref in zip(calls, alone):
+        assert torch.equal(torch.where(ref == T.SENT, ref, res), ref)
