@@ -280,7 +280,9 @@ la_status lora_decode_step_host(const la_attn_args* args, void* workspace,
  * On the tensor-core path (bf16, head_dim 128, r in {16, 32, 64}) the score
  * product takes the queries and each agent's keys K^a = K_base + delta in
  * fp16 (the sum rounded once): queries and keys must stay below 65504 in
- * magnitude there.
+ * magnitude there.  The delta is turned in fp16 before s joins it: LRk B_k^a
+ * (without s, its rotated pairs included) must stay below 65504 too, and so
+ * must s; an |s| below 2^-14 loses bits.
  * Errors: LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CAPACITY
  * (q_pos0 + n_q_tokens > L_max), LA_ERR_CUDA.
  */
@@ -453,8 +455,10 @@ typedef struct {
  * the caches.  Cache rows no node sees may hold anything, NaN included; the
  * rows of a tree's own nodes must be finite.  Outputs of nodes at or past
  * tree_len are left as they were.
- * With bf16 inputs the scores take queries and keys in fp16 as lora_attn_prefill
- * does (below 65504 in magnitude), except with B_k NULL, where they stay bf16.
+ * Roundings with bf16 inputs: scores take the queries, the key delta s LRk B_k^a
+ * (with its turns) and the keys K^a in fp16, each below 65504 in magnitude, whatever
+ * s is; with B_k NULL queries and keys stay bf16.  Softmax weights are rounded to
+ * bf16 before they weigh the values; sums, maxima and products are fp32.
  * No workspace: the key splits of a block are a thread-block cluster.
  * Errors: as lora_attn_prefill; LA_ERR_INVALID_ARG for a null tree, n_trees
  * neither 1 nor n_agents or n outside [1, LA_TREE_MAX_NODES];

@@ -7,7 +7,8 @@
 // cluster and merge over distributed shared memory.  Keys stream in tiles of
 // 128: the committed context, then one tile with the tree's own nodes.  Per tile
 //   dK  = LRk B_k^a                     tcgen05, half the frequencies at a time
-//   K^a = K_base + s R(k0) R(j) dK      CUDA cores, in fp16 over K_base
+//   K^a = K_base + s R(k0) R(j) dK      CUDA cores, in fp16 over K_base (dK carries s's
+//                                       power of two, through B_k^a)
 //   S   = Q K^a^T                       tcgen05, Q (fp16) read from TMEM
 //   P   = exp2(S log2e scale - m)       CUDA cores, bf16 to TMEM
 //   [O | O_lr] += P [V_base | LRv]      tcgen05, P read from TMEM
@@ -107,6 +108,17 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The power of two in s: B_k^a carries it (exactly, in bf16) and the anchors the rest, so
+// that fp16 holds s LRk B_k^a to a factor of two and neither s nor LRk B_k^a alone
+__device__ __forceinline__ float scale_pow2(float s) {
+  const uint32_t e = __float_as_uint(s) & 0x7f800000u;
+  return __uint_as_float(e ? e : 0x00800000u);
+}
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t v, float f) {
+  const __nv_bfloat162 h = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&v), __float2bfloat162_rn(f));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 template <int D, int R, bool KEYS>
 __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
     attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -121,7 +133,8 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
   const uint32_t sb = smem_u32(smem);
   const uint32_t k_u = sb, v_u = sb + C_::OFF_V, lrk_u = sb + C_::OFF_LRK, bk_u = sb + C_::OFF_BK;
   unsigned char* misc = smem + C_::OFF_MISC;
-  uint2* anc = reinterpret_cast<uint2*>(misc);   // [3][32]: s (cos, cos) and s (sin, sin) of two frequencies at k0, f16
+  uint2* anc = reinterpret_cast<uint2*>(misc);   // [3][32]: s (cos, cos) and s (sin, sin) of two frequencies at k0
+                                                 // (s without its power of two), f16
   float* xref = reinterpret_cast<float*>(misc + 1536);   // a row's reference maximum, handed between its two warps
   float* xsum = xref + QM;
   uint64_t* masks = reinterpret_cast<uint64_t*>(misc + 2560);
@@ -406,6 +419,7 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       // two adjacent frequencies a lane
       const int f = 2 * lane < H2 ? 2 * lane : 0;
       const double th0 = rt.theta[f], th1 = rt.theta[f + 1];
+      const float sm = p.s / scale_pow2(p.s);   // |sm| in [1, 2): B_k^a carries the rest
       setup_sync();
       int ks_ = 0, kp = 1;
       for (int i = 0; i < NT; ++i) {
@@ -413,8 +427,8 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
         const int64_t k0 = n0 + i == Nc ? C : (int64_t)(n0 + i) * KT;
         const float2 a = rope_cs_exact(k0, th0), b = rope_cs_exact(k0, th1);
         if (2 * lane < H2)
-          anc[ks_ * 32 + lane] = make_uint2(h2_bits(__floats2half2_rn(a.x * p.s, b.x * p.s)),
-                                            h2_bits(__floats2half2_rn(a.y * p.s, b.y * p.s)));
+          anc[ks_ * 32 + lane] = make_uint2(h2_bits(__floats2half2_rn(a.x * sm, b.x * sm)),
+                                            h2_bits(__floats2half2_rn(a.y * sm, b.y * sm)));
         __syncwarp();
         if (lane == 0) mbar_arrive(kfull(ks_));
         if (++ks_ == 3) { ks_ = 0; kp ^= 1; }
@@ -475,9 +489,11 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
 #pragma unroll
             for (int u = 0; u < NBK; ++u) {
               const int e = bt + u * 256, j = e / (D / 8), col = 8 * (e % (D / 8)), f = col % H2;
+              const uint4 v = bkv[u];
+              const float s2 = scale_pow2(p.s);
               if (e < R * D / 8)
                 sts128(bk_u + (uint32_t)(f / FP) * (R * FP * 4) + tile_off<2 * FP, R>(j, (col / H2) * FP + f % FP),
-                       bkv[u].x, bkv[u].y, bkv[u].z, bkv[u].w);
+                       scale_bf16x2(v.x, s2), scale_bf16x2(v.y, s2), scale_bf16x2(v.z, s2), scale_bf16x2(v.w, s2));
             }
             fence_proxy_async_smem();
             setup_sync();

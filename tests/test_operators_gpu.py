@@ -78,3 +78,22 @@ def test_kernels_with_tensor_memory_on_streams_of_their_own(la, keys):
     assert la.la_device_check() == la.LA_OK
     for (_, res), ref in zip(calls, alone):
         assert torch.equal(torch.where(ref == T.SENT, ref, res), ref)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("s,b_std", [(1.1e-5, 2e4), (3e5, 1e-6), (-0.75, 0.05), (2.0 ** -20, 3e5), (7e9, 3e-11), (0.0, 1.0)])
+def test_tree_takes_any_scale_the_delta_fits(la, d, s, b_std):
+    """Only K^a and the scaled delta have to lie in fp16's range, neither s nor LRk B_k^a
+    alone: deltas of about one from a small s and products beyond 65504, and the reverse.
+    (The bound of the trees' tests, on up-projections that carry s.)"""
+    i = T.make(d=d, r=16, ctx=(300,), n=7, garbage=False, seed=32)
+    s = float(np.float32(s))
+    gen = torch.Generator().manual_seed(33)
+    for k in ("B_k", "B_v"):
+        i[k] = (torch.randn(i[k].shape, generator=gen) * b_std).to(torch.bfloat16)
+    args, tree, out, keep = T.launch(la, i, torch.float32)
+    args.lora_scale = s
+    la.lora_attn_tree(args, tree)
+    torch.cuda.synchronize()
+    assert la.la_device_check() == la.LA_OK
+    T.check(la, {**i, **{k: i[k].double() * (s / 2.0) for k in ("B_k", "B_v")}}, out, torch.float32)   # its scale is 2
