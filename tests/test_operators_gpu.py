@@ -1,5 +1,7 @@
 """Calls of the drafted-tree operators that their documentation allows and no other test
 makes, against the fp64 oracle within the operators' own bounds."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -97,3 +99,39 @@ def test_tree_takes_any_scale_the_delta_fits(la, d, s, b_std):
     torch.cuda.synchronize()
     assert la.la_device_check() == la.LA_OK
     T.check(la, {**i, **{k: i[k].double() * (s / 2.0) for k in ("B_k", "B_v")}}, out, torch.float32)   # its scale is 2
+
+
+def in_threads(*works):
+    """Run every function in a host thread of its own, all at once; their errors."""
+    errors = []
+
+    def run(f):
+        try:
+            f()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(f,)) for f in works]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return errors
+
+
+def test_threads_with_different_ranks(la):
+    """Two host threads call at once, each with a rank (a shared-memory size) of its own."""
+    runs = []
+    for r in (8, 64):
+        i = T.make(dtype=torch.float32, d=64, r=r, ctx=(90,), n=4, garbage=False, seed=r)
+        runs.append((i, torch.cuda.Stream(), *T.launch(la, i, torch.float32)))
+    torch.cuda.synchronize()
+
+    def work(s, args, tree):
+        for _ in range(2000):
+            la.lora_attn_tree(args, tree, stream=s)
+
+    assert in_threads(*(lambda x=x: work(*x[1:4]) for x in runs)) == []
+    for i, s, args, tree, out, keep in runs:
+        T.check(la, i, out, torch.float32)
