@@ -64,17 +64,24 @@ __device__ __forceinline__ float2 sincos_small(float ang) {
   return make_float2(c, s);
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda)
+// A driver function through the runtime's entry point (no -lcuda)
+inline void* driver_fn(const char* name) {
+  void* ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  const bool ok = cudaGetDriverEntryPoint(name, &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+                  q == cudaDriverEntryPointSuccess;
+  return ok ? ptr : nullptr;
+}
+
+// cuTensorMapEncodeTiled, or null.  It wants a context, and a host thread whose first CUDA
+// work is this call has none yet: the current device's primary one is bound then.
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
+  static const auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_fn("cuTensorMapEncodeTiled"));
+  static const auto current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(driver_fn("cuCtxGetCurrent"));
+  CUcontext ctx = nullptr;
+  int dev = 0;
+  if (!fn || !current || current(&ctx) != CUDA_SUCCESS) return nullptr;
+  if (!ctx && (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)) return nullptr;
   return fn;
 }
 

@@ -135,3 +135,31 @@ def test_threads_with_different_ranks(la):
     assert in_threads(*(lambda x=x: work(*x[1:4]) for x in runs)) == []
     for i, s, args, tree, out, keep in runs:
         T.check(la, i, out, torch.float32)
+
+
+def test_first_cuda_call_of_a_thread(la):
+    """A host thread that has made no CUDA call before calls an entry point with tensor
+    maps: the thread has no context of its own yet."""
+    i = T.make(ctx=(90,), n=4, garbage=False, seed=34)
+    args, tree, out, keep = T.launch(la, i)
+    d = keep[0]
+    ref = torch.zeros_like(out)
+    pre = la.make_args(d["k_base"], d["v_base"], d["lr"], d["B_k"], d["B_v"], d["q"], ref, lora_scale=2.0,
+                       rope_base=i["base"], q_pos0=90)
+    q1 = d["q"][:, :, :1].contiguous()
+    dec = la.make_args(d["k_base"], d["v_base"], d["lr"], d["B_k"], d["B_v"], q1, torch.zeros_like(q1), lora_scale=2.0,
+                       rope_base=i["base"], kv_len=d["kv_len"], max_kv_len=94)
+    ws = la.decode_workspace(dec, DEV)
+    z = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    ss, sa = (torch.tensor(v, dtype=torch.int32, device=DEV) for v in ([0, 9], [0]))
+    ga = la.make_grouped_args(z(9, 64), z(64, 16), z(1, 16, 64), z(9, 64), z(9, 64), ss, sa, lora_scale=1.0)
+    X, A_kv, lr = z(1, 40, 256), z(256, 64), z(1, 40, 64)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda: la.lora_attn_tree(args, tree, stream=s), lambda: la.lora_attn_prefill(pre, stream=s),
+                 lambda: la.lora_attn_decode(dec, ws, stream=s), lambda: la.lora_grouped_delta(ga, stream=s),
+                 lambda: la.lr_cache_append(X, A_kv, lr, 0, stream=s)):
+        assert in_threads(call) == []
+    assert la.la_device_check() == la.LA_OK
+    T.check(la, i, out, torch.bfloat16)
+    assert (lr == 256).all() and (ga.keep[4] == 1 + 64 * 16).all()
