@@ -273,6 +273,16 @@ def lora_output_delta(o: torch.Tensor, A_o: torch.Tensor, B_o: torch.Tensor, y: 
     _check(st, "lora_output_delta")
 
 
+def _strides(t: torch.Tensor) -> list:
+    """t's strides, dense ones in place of those of dimensions with one entry, which are never
+    used and may hold anything."""
+    st = list(t.stride())
+    for i in range(t.dim() - 2, -1, -1):
+        if t.shape[i] <= 1:
+            st[i] = t.shape[i + 1] * st[i + 1]
+    return st
+
+
 def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_base: float,
               softmax_scale: Optional[float] = None, kv_len: Optional[torch.Tensor] = None,
               max_kv_len: int = 0, q_pos0: int = 0, value_path: int = LA_VALUE_REORDERED,
@@ -293,13 +303,13 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
     n_seqs, n_kv, L_max, d = k_base.shape
     n_agents, n_tok, n_q = q.shape[1], q.shape[2], q.shape[3]
     per_agent = lr.dim() == 4
-    lr_agent_stride = lr.stride(0) if per_agent else 0
+    lr_strides, kv_strides = _strides(lr), _strides(k_base)
+    lr_agent_stride = lr_strides[0] if per_agent else 0
     if per_agent:
         assert lr.shape[0] == n_agents
-        lr = lr[0]
-    r = lr.shape[2] // 2
-    assert k_base.stride() == v_base.stride() and k_base.stride(3) == 1
-    assert lr.stride(2) == 1 and lr.stride(1) == 2 * r
+    r = lr.shape[-1] // 2
+    assert kv_strides == _strides(v_base) and kv_strides[3] == 1
+    assert lr_strides[-2:] == [2 * r, 1]
     assert B_k is None or B_k.is_contiguous()
     assert B_v.is_contiguous() and q.is_contiguous() and out.is_contiguous()
     a = AttnArgs()
@@ -310,9 +320,8 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
     a.rope_base = rope_base
     a.L_max = L_max
     a.k_base, a.v_base = k_base.data_ptr(), v_base.data_ptr()
-    a.kv_seq_stride, a.kv_head_stride, a.kv_tok_stride = (k_base.stride(0), k_base.stride(1),
-                                                          k_base.stride(2))
-    a.lr_cache, a.lr_seq_stride = lr.data_ptr(), lr.stride(0)
+    a.kv_seq_stride, a.kv_head_stride, a.kv_tok_stride = kv_strides[:3]
+    a.lr_cache, a.lr_seq_stride = lr.data_ptr(), lr_strides[-3]
     a.B_k, a.B_v = (B_k.data_ptr() if B_k is not None else None), B_v.data_ptr()
     a.q, a.out = q.data_ptr(), out.data_ptr()
     a.kv_len = kv_len.data_ptr() if kv_len is not None else None
@@ -538,7 +547,7 @@ def make_qk_args(q, k, v, w_q, w_k, q_out, k_base, v_base, kv_len, *, rope_base:
             raise ValueError("q_out must be contiguous, of q's shape")
         a.n_agents, a.n_q_heads = q.shape[1], q.shape[3]
         a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
-        a.q_seq_stride, a.q_agent_stride, a.q_tok_stride = q.stride()[:3]
+        a.q_seq_stride, a.q_agent_stride, a.q_tok_stride = _strides(q)[:3]
     a.n_trees = None
     if k is not None:
         heads(k)
@@ -547,16 +556,16 @@ def make_qk_args(q, k, v, w_q, w_k, q_out, k_base, v_base, kv_len, *, rope_base:
             a.n_agents = k.shape[1]
         a.n_kv_heads = k.shape[3]
         a.k, a.v = k.data_ptr(), _ptr(v)
-        a.kv_in_seq_stride, a.kv_in_tree_stride, a.kv_in_tok_stride = k.stride()[:3]
+        a.kv_in_seq_stride, a.kv_in_tree_stride, a.kv_in_tok_stride = _strides(k)[:3]
         if k_base.dim() != 4 or k_base.shape[:2] != (n_seqs, a.n_kv_heads) or \
                 k_base.shape[3] != d or k_base.stride(3) != 1:
             raise ValueError("k_base must be [n_seqs, n_kv, L_max, d] with a unit last stride")
-        if v is not None and (v.shape != k.shape or v.stride() != k.stride() or
-                              v_base.shape != k_base.shape or v_base.stride() != k_base.stride()):
+        if v is not None and (v.shape != k.shape or _strides(v) != _strides(k) or v_base.shape != k_base.shape or
+                              _strides(v_base) != _strides(k_base)):
             raise ValueError("v and v_base must have the shapes and strides of k and k_base")
         a.k_base, a.v_base = k_base.data_ptr(), _ptr(v_base)
         a.L_max = k_base.shape[2]
-        a.kv_seq_stride, a.kv_head_stride, a.kv_tok_stride = k_base.stride()[:3]
+        a.kv_seq_stride, a.kv_head_stride, a.kv_tok_stride = _strides(k_base)[:3]
     elif v is not None:
         raise ValueError("v needs k")
     else:
@@ -613,7 +622,7 @@ def make_grouped_args(x, A, B, y, out, seg_start, seg_agent, *, lora_scale: floa
     a.n_tokens, a.hidden, a.n_out, a.r, a.n_agents, a.n_segs = T, H, N, r, n_agents, n_segs
     a.lora_scale = lora_scale
     a.x, a.ldx = x.data_ptr(), x.stride(0) if T > 1 else H
-    a.A, a.a_agent_stride = A.data_ptr(), (A.stride(0) if A.dim() == 3 else 0)
+    a.A, a.a_agent_stride = A.data_ptr(), (A.stride(0) if A.dim() == 3 and n_agents > 1 else 0)
     a.B = B.data_ptr()
     a.y, a.ldy = y.data_ptr(), y.stride(0) if T > 1 else N
     a.out, a.ldo = out.data_ptr(), out.stride(0) if T > 1 else N

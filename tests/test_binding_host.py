@@ -1,5 +1,6 @@
 """The Python binding's argument structs, on the CPU: tensors stand in for CUDA
 ones (the device check is replaced), nothing is launched."""
+import ctypes
 import gc
 import weakref
 
@@ -46,3 +47,46 @@ def test_structs_keep_their_tensors(any_device, name):
     del args
     gc.collect()
     assert all(x() is None for x in refs)
+
+
+def odd(t, dim):
+    """t with a meaningless stride in a dimension of one entry (as views of slices have)."""
+    st = list(t.stride())
+    assert t.shape[dim] == 1
+    st[dim] = 7
+    return t.as_strided(t.shape, st)
+
+
+def status(fn, args, *rest):
+    return getattr(la.lib, fn)(ctypes.byref(args), *rest)
+
+
+def test_strides_of_single_entries_are_not_looked_at(any_device):
+    """A stride of a dimension of one entry is never used, so it refuses nothing: the call
+    gets as far as a max_kv_len beyond L_max (nothing launches)."""
+    z = torch.zeros
+    kl = z(1, dtype=I32)
+    q, k, kb = z(1, 1, 1, 4, 64), z(1, 1, 1, 2, 64), z(1, 2, 16, 64)
+    for dim in range(3):
+        for t in (odd(q, dim),):
+            a = la.make_qk_args(t, k, k.clone(), None, None, z(1, 1, 1, 4, 64), kb, kb.clone(), kl, rope_base=1e4, max_kv_len=17)
+            assert status("lora_qk_norm_rope", a, None, None) == la.LA_ERR_CAPACITY
+        for kk, vv in ((odd(k, dim), odd(k, dim)), (k, odd(k, dim)), (odd(k, dim), k)):
+            a = la.make_qk_args(q, kk, vv, None, None, z(1, 1, 1, 4, 64), kb, kb.clone(), kl, rope_base=1e4, max_kv_len=17)
+            assert status("lora_qk_norm_rope", a, None, None) == la.LA_ERR_CAPACITY
+    for kc, vc in ((odd(kb, 0), kb.clone()), (kb, odd(kb, 0)), (odd(z(1, 1, 16, 64), 1), z(1, 1, 16, 64))):
+        a = la.make_qk_args(q, k[:, :, :, :kc.shape[1]], k[:, :, :, :kc.shape[1]].clone(), None, None,
+                            z(1, 1, 1, 4, 64), kc, vc, kl, rope_base=1e4, max_kv_len=17)
+        assert status("lora_qk_norm_rope", a, None, None) == la.LA_ERR_CAPACITY
+    x, A, B, y = z(5, 16), z(1, 16, 8), z(1, 8, 8), z(5, 8)
+    a = la.make_grouped_args(x, odd(A, 0), B, y, y, z(2, dtype=I32), z(1, dtype=I32), lora_scale=1.0)
+    assert a.a_agent_stride == 0   # one agent, one A
+
+
+def test_strides_of_several_entries_count(any_device):
+    z = torch.zeros
+    q, kb, kl = z(2, 1, 1, 4, 64), z(2, 2, 16, 64), z(2, dtype=I32)
+    k = z(2, 1, 1, 2, 64)
+    with pytest.raises(ValueError):
+        la.make_qk_args(q, k, z(2, 2, 1, 2, 64)[:, :1], None, None, z(2, 1, 1, 4, 64), kb, kb.clone(), kl,
+                        rope_base=1e4, max_kv_len=16)
