@@ -338,6 +338,7 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
     a.row_stats = row_stats.data_ptr() if row_stats is not None else None
     a.device = q.device.index
     a.keep = keep
+    a.checked = False   # lora_attn_tree's checks of these tensors, on its first call
     return a
 
 
@@ -496,10 +497,35 @@ def _check_tree(tree: TreeArgs, n_seqs: int, n: int, where: str) -> None:
                          f"n_seqs {n_seqs} and n {n}")
 
 
+def _check_attn(args: AttnArgs) -> None:
+    """The tensors behind make_args' struct: one type, one device, shapes that fit (the
+    struct alone does not show them)."""
+    k_base, v_base, lr, B_k, B_v, q, out, kv_len, _ = args.keep
+    n_seqs, n_kv, L_max, d = k_base.shape
+    n_agents, r = q.shape[1], lr.shape[-1] // 2
+    for t in (v_base, lr, B_k, B_v, q):
+        if t is not None and t.dtype != k_base.dtype:
+            raise TypeError(f"lora_attn_tree: expected every input of {k_base.dtype}, got {t.dtype}")
+    if kv_len is None or kv_len.dtype != torch.int32 or not kv_len.is_contiguous() or kv_len.numel() < n_seqs:
+        raise ValueError("lora_attn_tree: kv_len must be int32 [n_seqs]")
+
+    def holds(t, *shape):   # with room for more agents than the call has, if it likes
+        return t.dim() == len(shape) and t.shape[0] >= shape[0] and tuple(t.shape[1:]) == shape[1:]
+
+    if v_base.shape != k_base.shape or q.shape[0] != n_seqs or q.shape[4:] != (d,) or out.numel() < q.numel() or \
+            lr.shape[-3] < n_seqs or lr.shape[-2] < L_max or not holds(B_v, n_agents, r, n_kv * d) or \
+            (B_k is not None and not holds(B_k, n_agents, r, n_kv * d)):
+        raise ValueError("lora_attn_tree: shapes of the caches, LR rows, B_k, B_v, q and out do not fit")
+    _same_device(args.keep)
+
+
 def lora_attn_tree(args: AttnArgs, tree: TreeArgs, stream=None) -> None:
     """Attention of the drafted nodes over the committed context and their own
     branches.  args from make_args, with q and out [n_seqs, n_agents, n, n_q, d],
     kv_len the committed lengths and max_kv_len a bound on kv_len + n_trees * n."""
+    if not getattr(args, "checked", True):
+        _check_attn(args)
+        args.checked = True
     _check_tree(tree, args.n_seqs, args.n_q_tokens, "lora_attn_tree")
     device = getattr(args, "device", None)   # of make_args' tensors
     if tree.device not in (None, device):

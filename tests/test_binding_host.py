@@ -90,3 +90,31 @@ def test_strides_of_several_entries_count(any_device):
     with pytest.raises(ValueError):
         la.make_qk_args(q, k, z(2, 2, 1, 2, 64)[:, :1], None, None, z(2, 1, 1, 4, 64), kb, kb.clone(), kl,
                         rope_base=1e4, max_kv_len=16)
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(), None),
+    (dict(q=torch.bfloat16), TypeError), (dict(lr=torch.bfloat16), TypeError), (dict(B_v=torch.bfloat16), TypeError),
+    (dict(v_base=torch.bfloat16), TypeError), (dict(B_k=torch.bfloat16), TypeError),
+    (dict(kv_len=torch.int64), ValueError), (dict(kv_len=(0,)), ValueError), (dict(kv_len=None), ValueError),
+    (dict(q=(1, 2, 3, 4, 32)), ValueError), (dict(q=(2, 2, 3, 4, 64)), ValueError), (dict(out=(1, 2, 2, 4, 64)), ValueError),
+    (dict(lr=(1, 15, 16)), ValueError), (dict(B_v=(2, 8, 64)), ValueError), (dict(B_k=(1, 8, 128)), ValueError),
+])
+def test_tree_attention_looks_at_its_tensors(monkeypatch, change, error):
+    """make_args' struct shows neither types nor shapes: a float32 call's bfloat16 queries, or
+    lengths in 64 bits, would be read as what they are not, past their end."""
+    shapes = dict(k_base=(1, 2, 16, 64), v_base=(1, 2, 16, 64), lr=(1, 16, 16), B_k=(2, 8, 128), B_v=(2, 8, 128),
+                  q=(1, 2, 3, 4, 64), out=(1, 2, 3, 4, 64))
+    t = {k: torch.zeros(change[k] if isinstance(change.get(k), tuple) else s,
+                        dtype=change[k] if isinstance(change.get(k), torch.dtype) else torch.float32)
+         for k, s in shapes.items()}
+    c = change.get("kv_len", I32)
+    kl = None if c is None else torch.zeros(c if isinstance(c, tuple) else 1, dtype=c if isinstance(c, torch.dtype) else I32)
+    args = la.make_args(**t, lora_scale=1.0, rope_base=1e4, kv_len=kl, max_kv_len=17)   # beyond L_max: nothing launches
+    with pytest.raises(ValueError if error is None else error):
+        la.lora_attn_tree(args, la.make_tree_args(None))    # not on a CUDA device, or the change
+    if error is None:
+        monkeypatch.setattr(la, "_same_device", lambda ts: 0)
+        with pytest.raises(la.LoraAttnError) as e:
+            la.lora_attn_tree(args, la.make_tree_args(None), stream=0)
+        assert e.value.status == la.LA_ERR_CAPACITY
