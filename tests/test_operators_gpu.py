@@ -163,3 +163,58 @@ def test_first_cuda_call_of_a_thread(la):
     assert la.la_device_check() == la.LA_OK
     T.check(la, i, out, torch.bfloat16)
     assert (lr == 256).all() and (ga.keep[4] == 1 + 64 * 16).all()
+
+
+# ---- forms that no other test runs
+@pytest.mark.parametrize("r", [8, 16, 32, 64])
+@pytest.mark.parametrize("keys", [True, False])
+@pytest.mark.parametrize("n", [13, 27])   # folded, and with two warps a row
+def test_tree_head_dim_64_many_tiles(la, r, keys, n):
+    """head_dim 64 over long unsplit runs of tiles: both dK buffers, every K, V and LR stage
+    refilled many times, partial context tiles and drafted ones at their end."""
+    T.run(la, S=3, A=4, kv=8, g=4, d=64, r=r, ctx=(2999, 1777, 2421), n=n, per_agent=True, lens=(13, 9, 2, 7, 12),
+          keys=keys, seed=r + n)
+
+
+def test_tree_of_one_node_is_the_decode(la):
+    """Committed length C in front of one node is the decode of kv_len = C + 1, and a chain the
+    prefill: row and position conventions of three entry points, within the bf16 bound of the
+    library's paths (1e-2 of the largest output), over ranks and lengths off the tile."""
+    for r, ctx in ((16, (200, 77)), (64, (383, 1)), (32, (128, 1290))):
+        for n in (1, 9):
+            i = T.make(S=2, A=2, r=r, ctx=ctx, n=n, extra=0, garbage=False, seed=r + n)
+            i["parent"] = None
+            args, tree, out, keep = T.launch(la, i, torch.float32)
+            la.lora_attn_tree(args, tree)
+            d = keep[0]
+            caches = (d["k_base"], d["v_base"], d["lr"], d["B_k"], d["B_v"])
+            ref = torch.zeros_like(out)
+            if n == 1:
+                dec = la.make_args(*caches, d["q"], ref, lora_scale=2.0, rope_base=i["base"], kv_len=d["kv_len"] + 1,
+                                   max_kv_len=i["max_kv_len"])
+                la.lora_attn_decode(dec, la.decode_workspace(dec, DEV))
+            for s in range(2 if n > 1 else 0):   # one prefill a sequence: its first position is the host's
+                one = [x[s:s + 1] for x in caches[:3]]
+                la.lora_attn_prefill(la.make_args(*one, *caches[3:], d["q"][s:s + 1], ref[s:s + 1], lora_scale=2.0,
+                                                  rope_base=i["base"], q_pos0=ctx[s]))
+            torch.cuda.synchronize()
+            assert la.la_device_check() == la.LA_OK
+            T.check(la, i, out, torch.float32)
+            assert (out - ref).abs().max() <= 1e-2 * ref.abs().max(), (r, ctx, n)
+
+
+def test_tree_launches_in_a_row_over_every_form(la):
+    """Thirty launches give the same bits, head_dim 64 and rank 8 among them."""
+    for kw in (dict(d=64, r=16, n=13), dict(d=64, r=64, n=27), dict(d=64, r=32, n=27, keys=False), dict(d=128, r=8, n=13),
+               dict(d=64, r=8, n=5, lr_agents=True)):
+        i = T.make(S=4, A=3, kv=2, g=3, ctx=(1450, 700, 1101, 481), per_agent=True, garbage=False, seed=35, **kw)
+        args, tree, out, keep = T.launch(la, i)
+        la.lora_attn_tree(args, tree)
+        torch.cuda.synchronize()
+        T.check(la, i, out, torch.bfloat16)
+        first = out.clone()
+        for _ in range(30):
+            out.fill_(T.SENT)
+            la.lora_attn_tree(args, tree)
+            assert torch.equal(out, first), kw
+    assert la.la_device_check() == la.LA_OK
