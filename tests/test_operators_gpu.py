@@ -1,6 +1,7 @@
 """Calls of the drafted-tree operators that their documentation allows and no other test
 makes, against the fp64 oracle within the operators' own bounds."""
 import threading
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -218,3 +219,43 @@ def test_tree_launches_in_a_row_over_every_form(la):
             la.lora_attn_tree(args, tree)
             assert torch.equal(out, first), kw
     assert la.la_device_check() == la.LA_OK
+
+
+def test_readme_layer_runs(la):
+    """README's layer of a verification step, word for word, over a batch of two lengths."""
+    text = (Path(__file__).resolve().parent.parent / "README.md").read_text()
+    part = text.split("## Verifying drafted tokens")[1].split("\n## ")[0]
+    code = "\n".join(ln[4:] for ln in part.splitlines() if ln.startswith("    "))
+    assert "lora_attn_tree" in code and code.count("lora_grouped_delta") == 2
+    i = T.make(S=2, A=2, kv=2, g=2, d=64, r=16, ctx=(90, 41), n=5, lens=(5, 3), extra=0, garbage=False, seed=36, base=1e4)
+    args, tree, o, (dd, _, par, tl) = T.launch(la, i)
+    gen = torch.Generator(device=DEV).manual_seed(37)
+    f = lambda *s, std=1.0: (torch.randn(*s, generator=gen, device=DEV) * std).to(torch.bfloat16)  # noqa: E731
+    H, r, n, n_q, d, rows = 128, 16, 5, 4, 64, 20
+    seg_start, seg_agent = (torch.tensor(v, dtype=torch.int32, device=DEV) for v in ([0, 5, 10, 15, 20], [0, 1, 0, 1]))
+    env = dict(la=la, parent=par, tree_len=tl, n_q=n_q, d=d, x=f(rows, H), q=f(2, 2, n, n_q, d), A_q=f(H, r, std=H ** -0.5),
+               B_q=f(2, r, n_q * d, std=0.05), seg_start=seg_start, seg_agent=seg_agent, s=2.0, base=1e4, L=i["max_kv_len"],
+               k=f(2, 1, n, 2, d), v=f(2, 1, n, 2, d), w_q=None, w_k=None, q_rot=torch.zeros_like(dd["q"]),
+               k_base=dd["k_base"], v_base=dd["v_base"], kv_len=dd["kv_len"], lengths=i["kv_len"].tolist(),
+               x_tree=f(2, n, H), A_kv=f(H, 2 * r, std=H ** -0.5), lr_cache=dd["lr"], B_k=dd["B_k"], B_v=dd["B_v"], o=o,
+               A_o=f(2, n_q * d, r, std=0.05), B_o=f(2, r, H, std=0.05), y=f(rows, H), out=torch.zeros(rows, H, dtype=torch.bfloat16, device=DEV))
+    q0, lr0 = env["q"].clone(), dd["lr"].clone()
+    exec(code, env)
+    torch.cuda.synchronize()
+    assert la.la_device_check() == la.LA_OK
+    cuts, who = seg_start.tolist(), seg_agent.tolist()
+
+    def products(x, A, B, y, got):
+        ref = O.grouped_delta(x.cpu(), A.cpu(), B.cpu(), to_np(y), cuts, who, 2.0)
+        mag = O.grouped_delta(x.abs().cpu(), A.abs().cpu(), B.abs().cpu(), 0 * to_np(y), cuts, who, 2.0)
+        assert (np.abs(to_np(got) - ref) <= grouped_tol(ref, mag, to_np(y), x.shape[1], r, True)).all()
+
+    products(env["x"], env["A_q"], env["B_q"], q0.view(rows, -1), env["q"].view(rows, -1))
+    for s in range(2):   # the LR rows: at their places, the others as they were
+        C = env["lengths"][s]
+        want = env["x_tree"][s].double() @ env["A_kv"].double()
+        mag = env["x_tree"][s].abs().double() @ env["A_kv"].abs().double()
+        assert ((dd["lr"][s, C:C + n].double() - want).abs() <= 2.0 ** -8 * want.abs() + mag * (H + 8) * 2.0 ** -24).all()
+        assert torch.equal(dd["lr"][s, :C], lr0[s, :C]) and torch.equal(dd["lr"][s, C + n:], lr0[s, C + n:])
+    T.check(la, {**i, **{k: dd[k].cpu() for k in ("k_base", "v_base", "lr")}, "q": env["q_rot"].cpu()}, o, torch.bfloat16)
+    products(o.view(rows, -1), env["A_o"], env["B_o"], env["y"], env["out"])
