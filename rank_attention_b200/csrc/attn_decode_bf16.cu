@@ -67,7 +67,6 @@ constexpr int NES = 8;              // score warps (16 keys each)
 constexpr int NPV = 2;              // value warps
 constexpr int NTHR = 32 * (NES + NPV);
 constexpr int kMaxSplits = 32;
-constexpr int kSMs = 148;
 // named barriers (0 is __syncthreads)
 constexpr int BAR_MAX = 1, BAR_P = 2, BAR_PFREE = 4, BAR_QP = 6, BAR_END = 8;
 
@@ -1662,19 +1661,6 @@ size_t smem_for(const AttnParams& p) {
     case 32: return NT == 1 ? Cfg<128, 32, 1>::smem(na) : NT == 2 ? Cfg<128, 32, 2>::smem(na) : Cfg<128, 32, 3>::smem(na);
     default: return NT == 1 ? Cfg<128, 64, 1>::smem(na) : Cfg<128, 64, 2>::smem(na);
   }
-}
-
-// Splits per (sequence, KV head): enough CTAs for one CTA per SM.
-// SMs of the current device (148 on B200; also the answer when no device is
-// visible, so that workspace sizes can be planned on a host without a GPU)
-int device_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    return kSMs;
-  }
-  return n;
 }
 
 bool tc_fits(const AttnParams& p, int G);

@@ -356,8 +356,9 @@ cudaError_t launch_ts(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   const int QB = RB / p.g, nblk = (p.n_q_tokens + QB - 1) / QB;
   const int64_t units = (int64_t)nblk * p.n_agents * p.n_kv * p.n_seqs;
   const int64_t tiles = (p.max_kv_len + TK - 1) / TK + 1;
+  const int sms = device_sms();
   int S = 1;
-  while (S < 8 && units * S < 2 * 148 && tiles > S) S *= 2;
+  while (S < 8 && units * S < 2 * sms && tiles > S) S *= 2;
   p.n_splits = S;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, (unsigned)(nblk * p.n_agents * p.n_kv), (unsigned)p.n_seqs);

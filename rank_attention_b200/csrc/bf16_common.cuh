@@ -85,6 +85,18 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// SMs of the current device (148 on B200; also the answer when no device is
+// visible, so that workspace sizes can be planned on a host without a GPU)
+inline int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 148;
+  }
+  return n;
+}
+
 // the TMA swizzle whose span equals a box row of row_bytes (32, 64 or >= 128)
 inline CUtensorMapSwizzle swizzle_for(int row_bytes) {
   return row_bytes >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B

@@ -388,13 +388,14 @@ cudaError_t launch_gt(const GroupedParams& p, cudaStream_t st) {
   // The sum over distributed shared memory grows with CS: 16384 tokens, r 64, 132 tiles
   // at CS 1 / 2 / 4 / 8: 90 / 77 / 99 / 203 us; 1501 tokens, r 32, 21 tiles: 42 / 25 /
   // 17.8 / 18.9 us; 48 tokens, r 16, 4 tiles (one cluster a tile): 64 / 35 / 20 / 13 us.
+  const int sms = device_sms();
   int CS = 8;
-  while (CS > 2 && tiles * CS > 148) CS /= 2;
-  if (tiles * CS > 2 * 148) CS = 1;
+  while (CS > 2 && tiles * CS > sms) CS /= 2;
+  if (tiles * CS > 2 * sms) CS = 1;
   // clusters a tile: those that would otherwise leave SMs idle form t again and share
   // the columns, down to two blocks of 64 a CTA
   int Z = 1;
-  while (Z < 8 && tiles * CS * Z * 2 <= 148 && (int64_t)CS * Z * 4 * GC <= p.n_out) Z *= 2;
+  while (Z < 8 && tiles * CS * Z * 2 <= sms && (int64_t)CS * Z * 4 * GC <= p.n_out) Z *= 2;
   // as many stages as let two CTAs share an SM
   const int rest = 1024 + (CS > 1 ? C::RED : 0) + C::MISC;
   int ns = (113 * 1024 - rest) / C::STAGE;

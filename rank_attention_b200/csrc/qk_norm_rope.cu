@@ -238,7 +238,7 @@ cudaError_t launch_qk(const QkParams& pin, const TreeParams& tp, double rope_bas
   const int slots = p.q_slots + (p.k ? tp.n_trees : 0);
   // two tokens a CTA (one angle a thread at d = 128), one where that would leave
   // SMs without a CTA
-  p.tb = (int64_t)((p.n_tok + kMaxTB - 1) / kMaxTB) * slots * p.n_seqs >= 148 ? kMaxTB : 1;
+  p.tb = (int64_t)((p.n_tok + kMaxTB - 1) / kMaxTB) * slots * p.n_seqs >= device_sms() ? kMaxTB : 1;
   const dim3 grid((unsigned)((p.n_tok + p.tb - 1) / p.tb), (unsigned)slots, (unsigned)p.n_seqs);
   qk_norm_rope_kernel<IO, D><<<grid, NTH, 0, st>>>(p, tp, rt);
   return cudaGetLastError();
