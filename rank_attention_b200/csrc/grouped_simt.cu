@@ -297,6 +297,7 @@ extern "C" la_status lora_grouped_delta(const la_grouped_args* a, la_stream_t st
     return LA_ERR_INVALID_ARG;
   const int rows = grouped_tile_rows(a->dtype == LA_BF16, a->n_tokens, a->n_segs);
   if (grouped_tiles(a->n_tokens, a->n_segs, rows) > 65535) return LA_ERR_UNSUPPORTED;   // the grid's y
+  if (a->out == a->x || a->out == a->A || a->out == a->B) return LA_ERR_INVALID_ARG;   // read to the end
   GroupedParams p = {};
   p.x = a->x; p.ldx = a->ldx;
   p.y = a->y; p.ldy = a->ldy;

@@ -44,3 +44,10 @@ def test_queries_in_place_must_be_dense(kw, status):
 ])
 def test_grouped_refuses_more_tiles_than_the_grid_holds(kw):
     assert la.lib.lora_grouped_delta(ctypes.byref(grouped(**kw)), None) == UNS
+
+
+@pytest.mark.parametrize("kw", [dict(x=FAKE), dict(A=FAKE), dict(B=FAKE)])
+def test_grouped_refuses_out_over_an_input(kw):
+    """Only y may be out: the others are still read when the first columns are written."""
+    base = dict(x=OTHER, A=OTHER, B=OTHER, y=OTHER, out=FAKE)
+    assert la.lib.lora_grouped_delta(ctypes.byref(grouped(**{**base, **kw})), None) == BAD
