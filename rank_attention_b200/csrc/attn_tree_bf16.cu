@@ -108,11 +108,16 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The power of two in s: B_k^a carries it (exactly, in bf16) and the anchors the rest, so
-// that fp16 holds s LRk B_k^a to a factor of two and neither s nor LRk B_k^a alone
+// s as a power of two, which B_k^a carries (exactly, in bf16), and the rest, in [1, 2) or
+// (-2, -1], for the anchors: so fp16 holds s LRk B_k^a to a factor of two and neither s nor
+// LRk B_k^a alone.  An s below the normal numbers counts as (s 2^126) 2^-126.
 __device__ __forceinline__ float scale_pow2(float s) {
   const uint32_t e = __float_as_uint(s) & 0x7f800000u;
   return __uint_as_float(e ? e : 0x00800000u);
+}
+__device__ __forceinline__ float scale_rest(float s) {
+  const uint32_t b = __float_as_uint(s);
+  return b & 0x7f800000u ? __uint_as_float((b & 0x807fffffu) | 0x3f800000u) : s * 0x1p126f;
 }
 __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t v, float f) {
   const __nv_bfloat162 h = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&v), __float2bfloat162_rn(f));
@@ -419,8 +424,8 @@ __global__ void __launch_bounds__(TCfg<D, R, KEYS>::NTHR, 1)
       // two adjacent frequencies a lane
       const int f = 2 * lane < H2 ? 2 * lane : 0;
       const double th0 = rt.theta[f], th1 = rt.theta[f + 1];
-      const float sm = p.s / scale_pow2(p.s);   // |sm| in [1, 2): B_k^a carries the rest
       setup_sync();
+      const float sm = scale_rest(p.s);
       int ks_ = 0, kp = 1;
       for (int i = 0; i < NT; ++i) {
         if (i >= 3 && !mbar_wait(kaready(ks_), kp)) fail = 1;   // build(i - 3) has read its slot
