@@ -416,7 +416,8 @@ la_status lora_output_delta(const void* o, const void* A_o, int64_t a_agent_stri
  * ------------------------------------------------------------------------
  * One layer of a verification step is lora_grouped_delta (the agents'
  * projections), lora_qk_norm_rope (queries rotated, the drafted tokens' base
- * rows cached), lr_cache_append (their LR rows), lora_attn_tree, and
+ * rows cached), lr_cache_append (their LR rows; its position is the host's, so
+ * sequences of different committed lengths take a call each), lora_attn_tree, and
  * lora_grouped_delta again (the output projection).
  *
  * Sequence s has a committed length C = kv_len[s] >= 0 and n_trees trees of
@@ -453,7 +454,7 @@ typedef struct {
  * q_pos0 is ignored; value_path must be LA_VALUE_REORDERED, key_pos0 0 and
  * row_stats NULL.  The nodes' base K (rotated), base V and LR rows must be in
  * the caches.  Cache rows no node sees may hold anything, NaN included; the
- * rows of a tree's own nodes must be finite.  Outputs of nodes at or past
+ * rows of a tree's own nodes must be finite (values below 2^100).  Outputs of nodes at or past
  * tree_len are left as they were.
  * Roundings with bf16 inputs: scores take the queries, the key delta s LRk B_k^a
  * (with its turns) and the keys K^a in fp16, each below 65504 in magnitude, whatever
@@ -503,7 +504,7 @@ typedef struct {
  *   k_base[s][h][row] = RoPE_pos( norm(k[s][t][j][h], w_k) )
  *   v_base[s][h][row] = v[s][t][j][h]
  * with norm(x, w) = x / sqrt(mean(x^2) + eps) * w over the head dimension
- * (statistics in fp32), RoPE as for the keys of the caches, and rows and
+ * (statistics in fp32: sum x^2 has to lie in its range), RoPE as for the keys of the caches, and rows and
  * positions of the tree above; tree NULL is one chain per sequence: token j in
  * row and at position kv_len[s] + j (a decode token, or a prompt chunk of any
  * length).  Rows of tokens at or past tree_len are left as they were, in
@@ -582,7 +583,8 @@ la_status lora_attn_decode_static_scratch(const la_attn_args* args, la_stream_t 
  *
  * la_device_check_word -- the same, and writes the word's bits to *word
  * (host pointer; 0 when nothing fired):
- *   LA_DEV_KV_LEN     a decode kv_len[q] outside [1, max_kv_len]
+ *   LA_DEV_KV_LEN     a decode kv_len[q] outside [1, max_kv_len], or a committed
+ *                     length whose drafted rows would pass max_kv_len
  *   LA_DEV_PIPE_WAIT  a tensor-core kernel's wait on its copy/MMA pipeline
  *                     gave up after its iteration limit (the CTA skipped its
  *                     output and, holding TMEM, freed it)

@@ -16,9 +16,9 @@
 // rows, only those with rows of the tile; the other rows of a stage hold anything
 // (rows do not mix).  Bound by memory for many rows (x, y and out once each; A_a
 // and B_a come from L2), by latency for few: the cluster spreads a short segment
-// over CS SMs.  Hidden and out 4096: 16384 tokens, r 64, 407 MB, 77 us (5.3 TB/s, 81 %
-// of the copy rate; 84 us with inputs that change from call to call); 48 tokens, r 16,
-// 9.1 us; on the CUDA cores 1604 and 76 us.
+// over CS SMs.  Hidden and out 4096: 16384 tokens, r 64, 407 MB, 84 us with fresh inputs
+// (4.9 TB/s, 74 % of the copy rate; 77 us where calls repeat their inputs, part of which
+// is still in L2); 48 tokens, r 16, 9.1 us; on the CUDA cores 1604 and 76 us.
 //
 // Warps: four epilogue warps (a row a thread), one to issue the MMAs, one to load.
 #include <cuda.h>
