@@ -276,11 +276,15 @@ def lora_output_delta(o: torch.Tensor, A_o: torch.Tensor, B_o: torch.Tensor, y: 
 def _strides(t: torch.Tensor) -> list:
     """t's strides, dense ones in place of those of dimensions with one entry, which are never
     used and may hold anything."""
-    st = list(t.stride())
-    for i in range(t.dim() - 2, -1, -1):
-        if t.shape[i] <= 1:
-            st[i] = t.shape[i + 1] * st[i + 1]
+    shape, st = t.shape, list(t.stride())
+    for i in range(len(st) - 2, -1, -1):
+        if shape[i] <= 1:
+            st[i] = shape[i + 1] * st[i + 1]
     return st
+
+
+def _same_strides(a: torch.Tensor, b: torch.Tensor) -> bool:
+    return a.stride() == b.stride() or _strides(a) == _strides(b)
 
 
 def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_base: float,
@@ -308,7 +312,7 @@ def make_args(k_base, v_base, lr, B_k, B_v, q, out, *, lora_scale: float, rope_b
     if per_agent:
         assert lr.shape[0] == n_agents
     r = lr.shape[-1] // 2
-    assert kv_strides == _strides(v_base) and kv_strides[3] == 1
+    assert _same_strides(k_base, v_base) and kv_strides[3] == 1
     assert lr_strides[-2:] == [2 * r, 1]
     assert B_k is None or B_k.is_contiguous()
     assert B_v.is_contiguous() and q.is_contiguous() and out.is_contiguous()
@@ -586,8 +590,8 @@ def make_qk_args(q, k, v, w_q, w_k, q_out, k_base, v_base, kv_len, *, rope_base:
         if k_base.dim() != 4 or k_base.shape[:2] != (n_seqs, a.n_kv_heads) or \
                 k_base.shape[3] != d or k_base.stride(3) != 1:
             raise ValueError("k_base must be [n_seqs, n_kv, L_max, d] with a unit last stride")
-        if v is not None and (v.shape != k.shape or _strides(v) != _strides(k) or v_base.shape != k_base.shape or
-                              _strides(v_base) != _strides(k_base)):
+        if v is not None and (v.shape != k.shape or not _same_strides(v, k) or v_base.shape != k_base.shape or
+                              not _same_strides(v_base, k_base)):
             raise ValueError("v and v_base must have the shapes and strides of k and k_base")
         a.k_base, a.v_base = k_base.data_ptr(), _ptr(v_base)
         a.L_max = k_base.shape[2]
