@@ -1703,7 +1703,7 @@ cudaError_t launch_t(const AttnParams& p, cudaStream_t st) {
   if (!make_maps(p, &mk, &mv, &ml)) return cudaErrorInvalidValue;
   const size_t sm = C::smem(p.n_agents);
   auto kern = decode_bf16_kernel<D, R, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  cudaError_t e = allow_smem(kern, sm);
   if (e != cudaSuccess) return e;
   dim3 grid(p.n_splits, p.n_seqs * p.n_kv);
   kern<<<grid, NTHR, sm, st>>>(mk, mv, ml, p, rt);
@@ -1789,7 +1789,7 @@ cudaError_t launch_tc(const AttnParams& p, cudaStream_t st) {
   static_assert(TC_COLS < 512 || C::smem(1) >= kSmemAllTmem, "kept apart from other kernels with TMEM");
   const size_t sm = C::smem(p.agent_group);
   auto kern = decode_tc_kernel<D, R, NT, PA>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  cudaError_t e = allow_smem(kern, sm);
   if (e != cudaSuccess) return e;
   dim3 grid(p.n_splits, (p.n_agents + p.agent_group - 1) / p.agent_group, p.n_seqs * p.n_kv);
   // with split keys the unit's CTAs wait for one another: all must be resident

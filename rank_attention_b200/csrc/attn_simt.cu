@@ -348,8 +348,7 @@ cudaError_t launch_typed(const AttnParams& p, cudaStream_t st) {
   const int rows_cap = qb * p.rows_per_tok;
   SmemLayout L(rows_cap, p.d, p.r, p.lr_agent ? p.n_agents : 1);
   if (L.total > 227 * 1024) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<IO, OUT, NAIVE>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.total);
+  cudaError_t e = allow_smem(attn_simt_kernel<IO, OUT, NAIVE>, L.total);
   if (e != cudaSuccess) return e;
   const int units = p.n_seqs * p.n_kv;
   dim3 grid(p.decode ? p.n_splits : 1, p.decode ? 1 : (p.n_q_tokens + qb - 1) / qb, units);

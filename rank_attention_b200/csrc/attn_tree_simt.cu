@@ -348,8 +348,7 @@ cudaError_t launch_ts(const AttnParams& pin, const TreeParams& tp, cudaStream_t 
   rope_thetas(p.rope_base, D, &rt);
   const TsCfg<D> L(p.r);
   const auto kern = attn_tree_simt_kernel<OUT, D>;
-  // the largest rank's size whatever this call's: another thread's call may set it meanwhile
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TsCfg<D>(64).total);
+  cudaError_t e = allow_smem(kern, L.total);
   if (e != cudaSuccess) return e;
   // splits: enough CTAs for two an SM, at least a tile a split, at most the
   // portable cluster size

@@ -87,6 +87,15 @@ struct DecodePlan {
   int groups;              // agent groups of the tensor-core decode (1 otherwise)
 };
 
+// Lets a kernel ask for up to `need` bytes of dynamic shared memory.  The limit is set to
+// the same value by every call (226 KB; a device block has 227 with its static part), so
+// that a call of another thread with a smaller need cannot lower it before this launch.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t need) {
+  const size_t all = 226 * 1024;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(need > all ? need : all));
+}
+
 // ---------------------------------------------------------------------------
 // small device helpers
 // ---------------------------------------------------------------------------

@@ -138,6 +138,36 @@ def test_threads_with_different_ranks(la):
         T.check(la, i, out, torch.float32)
 
 
+def test_threads_with_different_shapes_of_prefill_and_decode(la):
+    """The same for the prefill and decode kernels whose shared memory goes by the call."""
+    def prepared(decode, **kw):
+        i = T.make(ctx=(90,), n=1 if decode else 4, garbage=False, **kw)
+        d = {k: (v.to(DEV) if isinstance(v, torch.Tensor) else v) for k, v in i.items()}
+        out = torch.zeros(d["q"].shape, dtype=torch.float32, device=DEV)
+        args = la.make_args(d["k_base"], d["v_base"], d["lr"], d["B_k"], d["B_v"], d["q"], out, lora_scale=2.0,
+                            rope_base=i["base"], kv_len=d["kv_len"] + 1, max_kv_len=91, q_pos0=90)
+        ws, s = la.decode_workspace(args, DEV) if decode else None, torch.cuda.Stream()
+
+        def work(n=1000):
+            for _ in range(n):
+                la.lora_attn_decode(args, ws, stream=s) if decode else la.lora_attn_prefill(args, stream=s)
+
+        work(1)
+        torch.cuda.synchronize()
+        return work, out, out.clone()
+
+    f32 = torch.float32
+    for decode, kws in ((False, (dict(dtype=f32, d=64, r=8, A=1, g=1), dict(dtype=f32, d=64, r=64, A=2, g=4))),
+                        (True, (dict(dtype=f32, d=64, r=8, A=1, g=1), dict(dtype=f32, d=64, r=64, A=2, g=4))),
+                        (True, (dict(r=16, A=1, g=4), dict(r=16, A=3, g=4))),      # tensor-core decode
+                        (True, (dict(r=8, A=1, g=4), dict(r=8, A=2, g=4)))):       # bf16, r = 8
+        runs = [prepared(decode, seed=40 + j, **kw) for j, kw in enumerate(kws)]
+        assert in_threads(*(w for w, _, _ in runs)) == [], (decode, kws)
+        for _, out, ref in runs:
+            assert (out - ref).abs().max() <= 1e-5 * ref.abs().max()
+    assert la.la_device_check() == la.LA_OK
+
+
 def test_first_cuda_call_of_a_thread(la):
     """A host thread that has made no CUDA call before calls an entry point with tensor
     maps: the thread has no context of its own yet."""
